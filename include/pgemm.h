@@ -387,6 +387,60 @@ int pgemm_tile_coords(int64_t t, int64_t n_m, int64_t n_n, int group_m, int cu_c
  * resets it -- so any other value means a launch was cut short. */
 int pgemm_read_work_counter(pgemm_handle_t h, int32_t* value);
 
+/* ---- token rows to their experts and back ------------------------------ */
+/*
+ * The steps around the per-expert products of a mixture-of-experts layer.
+ * T tokens name k experts each; slot s = t*k + j is choice j of token t,
+ * n = T*k. A slot whose id lies outside [0, E) is dropped: it has no row, no
+ * share in any sum and no gradient, whatever its weight holds. Kept slots are
+ * sorted by expert, slots of one expert in slot order (a stable sort, so
+ * every result is the same on every run):
+ *   offsets[e]  first sorted row of expert e, e = 0..E; offsets[E] = kept slots
+ *   order[p]    slot of sorted row p, -1 for p >= offsets[E]
+ *   pos[s]      sorted row of slot s, -1 for a dropped slot
+ * All three are int32 device arrays. dtype is PGEMM_F16 or PGEMM_BF16; rows
+ * are 16-bit elements, ld* is the distance of two rows in elements (0 repeats
+ * one row; it may be smaller or larger than H), outputs are contiguous. Sums
+ * are fp32, rounded once to nearest even. Rows of any length and any even
+ * address are taken; those of a multiple of 8 elements at 16-byte addresses
+ * are the fastest. All work is enqueued on the handle's stream; nothing is
+ * allocated. Entries of pos outside [0, n) count as dropped.
+ * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
+ * k < 1, E < 1, an unknown type or too small a workspace;
+ * PGEMM_ERR_UNSUPPORTED for n or H above 2^30 or E above 1024. */
+
+/* Integer type of the expert ids. */
+typedef enum { PGEMM_IDS_I32 = 0, PGEMM_IDS_I64 = 1 } pgemm_ids_t;
+
+/* Bytes of device scratch that pgemm_moe_dispatch needs for these sizes (0
+ * for few slots). A pure function. */
+int pgemm_moe_dispatch_workspace(int64_t T, int64_t k, int64_t E, int64_t* bytes);
+
+/* Sort the slots and move the rows: xs[p] = x[order[p] / k], zeros where
+ * order[p] = -1. x: T rows of H; ids: [T, k] contiguous; xs: [n, H]. offsets
+ * is written for T = 0 too. `work` is device memory of at least the bytes
+ * above, free again once the call's work is done. */
+int pgemm_moe_dispatch(pgemm_handle_t h, const void* x, int64_t ldx, const void* ids, int ids_type, int64_t T, int64_t k,
+                       int64_t E, int64_t H, int dtype, int32_t* offsets, int32_t* order, int32_t* pos, void* xs,
+                       void* work, int64_t work_bytes);
+
+/* Gradient of the rows: dx[t] = sum of dxs[pos[t*k + j]] over the token's
+ * kept slots, in the order of j. dxs: n rows of H; dx: [T, H]. */
+int pgemm_moe_dispatch_backward(pgemm_handle_t h, const void* dxs, int64_t lddxs, const int32_t* pos, int64_t T,
+                                int64_t k, int64_t H, int dtype, void* dx);
+
+/* Back to the tokens: out[t] = sum of w[t*k + j] * ys[pos[t*k + j]] over the
+ * token's kept slots. ys: n rows of H; w: [T, k] fp32; out: [T, H]. */
+int pgemm_moe_combine(pgemm_handle_t h, const void* ys, int64_t ldys, const float* w, const int32_t* pos, int64_t T,
+                      int64_t k, int64_t H, int dtype, void* out);
+
+/* Its gradients: dys[pos[s]] = w[s] * dout[t] (zeros in the rows from
+ * offsets[E] on) and dw[s] = <ys[pos[s]], dout[t]> in fp32 (0 for a dropped
+ * slot), s = t*k + j. dout: T rows of H; dys: [n, H]; dw: [T, k]. */
+int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
+                               const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
+                               int64_t E, int64_t H, int dtype, void* dys, float* dw);
+
 /* Benchmark aid, not part of the GEMM: make about `n_cus` CUs of device
  * `device` unavailable for about `microseconds`, asynchronously on the HIP
  * stream `hip_stream` (NULL = null stream). It launches n_cus workgroups

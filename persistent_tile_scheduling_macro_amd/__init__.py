@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpgemm.so")
@@ -37,6 +38,9 @@ PGEMM_TILE_128 = 2
 
 PGEMM_B_KN = 0
 PGEMM_B_NK = 1
+
+PGEMM_IDS_I32 = 0
+PGEMM_IDS_I64 = 1
 
 PGEMM_MAINLOOP_AUTO = 0
 PGEMM_MAINLOOP_LOCKSTEP = 1
@@ -87,6 +91,13 @@ _set_mainloop = _sig("pgemm_set_mainloop", _int, _vp, _int)
 _set_fp8_scales = _sig("pgemm_set_fp8_scales", _int, _vp, ctypes.c_float, ctypes.c_float)
 _tile_coords = _sig("pgemm_tile_coords", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
 _read_work_counter = _sig("pgemm_read_work_counter", _int, _vp, ctypes.POINTER(_i32))
+_moe_dispatch_workspace = _sig("pgemm_moe_dispatch_workspace", _int, _i64, _i64, _i64, ctypes.POINTER(_i64))
+_moe_dispatch = _sig("pgemm_moe_dispatch", _int, _vp, _vp, _i64, _vp, _int, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp,
+                     _vp, _vp, _i64)
+_moe_dispatch_backward = _sig("pgemm_moe_dispatch_backward", _int, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _int, _vp)
+_moe_combine = _sig("pgemm_moe_combine", _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp)
+_moe_combine_backward = _sig("pgemm_moe_combine_backward", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                             _i64, _i64, _int, _vp, _vp)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
 
@@ -262,6 +273,62 @@ def pgemm_read_work_counter(h) -> int:
 def pgemm_hold_cus(stream, device: int, n_cus: int, microseconds: int) -> None:
     """Benchmark aid: hold about n_cus CUs for about `microseconds` on `stream`."""
     _check(_hold_cus(_stream_ptr(stream), int(device), int(n_cus), int(microseconds)))
+
+
+def pgemm_moe_dispatch_workspace(T: int, k: int, E: int) -> int:
+    """Bytes of device scratch that pgemm_moe_dispatch needs."""
+    v = _i64()
+    _check(_moe_dispatch_workspace(int(T), int(k), int(E), ctypes.byref(v)))
+    return v.value
+
+
+def pgemm_moe_dispatch(h, x, ldx: int, ids, ids_type: int, T: int, k: int, E: int, H: int, dtype: int, offsets, order,
+                       pos, xs, work=None, work_bytes: int = 0) -> None:
+    """Sort T*k slots by expert and move the token rows (pointers or tensors)."""
+    _check(_moe_dispatch(h, _ptr(x), ldx, _ptr(ids), ids_type, T, k, E, H, dtype, _ptr(offsets), _ptr(order), _ptr(pos),
+                         _ptr(xs), _ptr(work), work_bytes), h)
+
+
+def pgemm_moe_dispatch_backward(h, dxs, lddxs: int, pos, T: int, k: int, H: int, dtype: int, dx) -> None:
+    _check(_moe_dispatch_backward(h, _ptr(dxs), lddxs, _ptr(pos), T, k, H, dtype, _ptr(dx)), h)
+
+
+def pgemm_moe_combine(h, ys, ldys: int, w, pos, T: int, k: int, H: int, dtype: int, out) -> None:
+    _check(_moe_combine(h, _ptr(ys), ldys, _ptr(w), _ptr(pos), T, k, H, dtype, _ptr(out)), h)
+
+
+def pgemm_moe_combine_backward(h, dout, lddout: int, ys, ldys: int, w, offsets, pos, T: int, k: int, E: int, H: int,
+                               dtype: int, dys, dw) -> None:
+    _check(_moe_combine_backward(h, _ptr(dout), lddout, _ptr(ys), ldys, _ptr(w), _ptr(offsets), _ptr(pos), T, k, E, H,
+                                 dtype, _ptr(dys), _ptr(dw)), h)
+
+
+_per_thread = threading.local()
+
+
+def thread_handle(device):
+    """The calling thread's own handle on a torch device, bound to torch's current stream there.
+
+    The operators of ``moe`` and ``w4`` use it when they are given none. It is created at the thread's first
+    such call on the device, which therefore must not be made under graph capture, and lives as long as the process.
+    """
+    import torch
+
+    index = device.index
+    if index is None:
+        index = torch.cuda.current_device()
+    handles = getattr(_per_thread, "handles", None)
+    if handles is None:
+        handles = _per_thread.handles = {}
+    h = handles.get(index)
+    if h is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call the operator once outside graph capture first: its handle is created then")
+        before = torch.cuda.current_device()
+        h = handles[index] = pgemm_create(index)
+        torch.cuda.set_device(before)  # pgemm_create makes its device current
+    _check(_set_stream(h, torch.cuda.current_stream(index).cuda_stream), h)
+    return h
 
 
 def matmul(A, B, C=None, *, sched: str | int = "static", grid_multiple: int = 0, handle=None):

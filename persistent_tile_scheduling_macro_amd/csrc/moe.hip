@@ -1,0 +1,250 @@
+// Entry points that sort token rows by expert and bring them back.
+#include "context.h"
+#include "moe_rows.h"
+
+using namespace pgemm;
+
+namespace {
+
+// Up to this many slots dispatch is one launch (dispatch_small_kernel), above it three.
+constexpr int64_t kSmallSlots = 2048;
+// Workgroups that clear the rows of dropped slots (they leave at once if there are none).
+constexpr int kClearBlocks = 128;
+
+int check_rows(pgemm_ctx* h, int64_t T, int64_t k, int64_t H, int dtype) {
+  if (T < 0 || k < 1 || H < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "sizes T=%lld k=%lld H=%lld", (long long)T, (long long)k, (long long)H);
+  if (T > INT32_MAX || k > INT32_MAX || T * k > (int64_t)1 << 30 || H > (int64_t)1 << 30)
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "T * k and H must not exceed 2^30");
+  if (dtype != PGEMM_F16 && dtype != PGEMM_BF16)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
+  return PGEMM_OK;
+}
+
+int check_experts(pgemm_ctx* h, int64_t E) {
+  if (E < 1) return fail(h, PGEMM_ERR_INVALID_ARG, "E=%lld experts", (long long)E);
+  if (E > moe::kMaxExperts)
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "E=%lld experts, at most %d", (long long)E, moe::kMaxExperts);
+  return PGEMM_OK;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+
+// Slots a workgroup of the sort takes: kTile, or more where that would make too many workgroups.
+int64_t sort_chunk(int64_t n) {
+  const int64_t tiles = (n + moe::kTile - 1) / moe::kTile;
+  return (tiles + moe::kMaxChunks - 1) / moe::kMaxChunks * moe::kTile;
+}
+
+// One wave carries a row of up to 1024 elements (two passes of 16 bytes a lane), four waves a longer one.
+int lanes_of(int64_t H) { return H > 1024 ? 256 : 64; }
+unsigned token_blocks(int64_t T, int64_t H) {
+  const int64_t per = moe::kThreads / lanes_of(H);
+  return (unsigned)((T + per - 1) / per);
+}
+
+template <class ID>
+void launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, bool al) {
+  const hipStream_t st = h->stream;
+  if (s.n <= kSmallSlots) {
+    auto kern = al ? moe::dispatch_small_kernel<ID, true> : moe::dispatch_small_kernel<ID, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)a.T + 1), dim3(moe::kThreads), 0, st, s, a);
+    return;
+  }
+  const int chunks = (int)((s.n + s.chunk - 1) / s.chunk);
+  hipLaunchKernelGGL(moe::sort_count_kernel<ID>, dim3(chunks), dim3(moe::kThreads), 0, st, s);
+  hipLaunchKernelGGL(moe::sort_place_kernel<ID>, dim3(chunks), dim3(moe::kThreads), 0, st, s, chunks);
+  if (a.H == 0) return;
+  a.token_blocks = (int)token_blocks(a.T, a.H);
+  const dim3 grid((unsigned)a.token_blocks + kClearBlocks);
+  const bool wide = lanes_of(a.H) == 256;
+  auto kern = al ? (wide ? moe::move_kernel<true, 256> : moe::move_kernel<true, 64>)
+                 : (wide ? moe::move_kernel<false, 256> : moe::move_kernel<false, 64>);
+  hipLaunchKernelGGL(kern, grid, dim3(moe::kThreads), 0, st, a);
+}
+
+template <int DT, bool AL, int LANES, bool WEIGHTED>
+void launch_sum_k(pgemm_ctx* h, const moe::SumArgs& a, unsigned grid) {
+  auto kern = a.k >= 8   ? moe::gather_sum_kernel<DT, AL, LANES, 8, WEIGHTED>
+              : a.k >= 3 ? moe::gather_sum_kernel<DT, AL, LANES, 4, WEIGHTED>
+                         : moe::gather_sum_kernel<DT, AL, LANES, 2, WEIGHTED>;
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
+}
+
+template <bool WEIGHTED>
+void launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int dtype, bool al) {
+  const unsigned grid = token_blocks(a.T, a.H);
+  const int form = (dtype == PGEMM_BF16 ? 4 : 0) + (al ? 2 : 0) + (lanes_of(a.H) == 256 ? 1 : 0);
+  switch (form) {
+    case 0: return launch_sum_k<kF16, false, 64, WEIGHTED>(h, a, grid);
+    case 1: return launch_sum_k<kF16, false, 256, WEIGHTED>(h, a, grid);
+    case 2: return launch_sum_k<kF16, true, 64, WEIGHTED>(h, a, grid);
+    case 3: return launch_sum_k<kF16, true, 256, WEIGHTED>(h, a, grid);
+    case 4: return launch_sum_k<kBF16, false, 64, WEIGHTED>(h, a, grid);
+    case 5: return launch_sum_k<kBF16, false, 256, WEIGHTED>(h, a, grid);
+    case 6: return launch_sum_k<kBF16, true, 64, WEIGHTED>(h, a, grid);
+    default: return launch_sum_k<kBF16, true, 256, WEIGHTED>(h, a, grid);
+  }
+}
+
+template <int DT, bool AL, int LANES>
+void launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
+  auto kern = a.k >= 8   ? moe::combine_backward_kernel<DT, AL, LANES, 8>
+              : a.k >= 3 ? moe::combine_backward_kernel<DT, AL, LANES, 4>
+                         : moe::combine_backward_kernel<DT, AL, LANES, 2>;
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
+}
+
+void launch_back(pgemm_ctx* h, const moe::BackArgs& a, int dtype, bool al) {
+  const unsigned grid = (unsigned)a.token_blocks + kClearBlocks;
+  const int form = (dtype == PGEMM_BF16 ? 4 : 0) + (al ? 2 : 0) + (lanes_of(a.H) == 256 ? 1 : 0);
+  switch (form) {
+    case 0: return launch_back_k<kF16, false, 64>(h, a, grid);
+    case 1: return launch_back_k<kF16, false, 256>(h, a, grid);
+    case 2: return launch_back_k<kF16, true, 64>(h, a, grid);
+    case 3: return launch_back_k<kF16, true, 256>(h, a, grid);
+    case 4: return launch_back_k<kBF16, false, 64>(h, a, grid);
+    case 5: return launch_back_k<kBF16, false, 256>(h, a, grid);
+    case 6: return launch_back_k<kBF16, true, 64>(h, a, grid);
+    default: return launch_back_k<kBF16, true, 256>(h, a, grid);
+  }
+}
+
+int sum_impl(pgemm_handle_t h, const void* rows, int64_t ld, const float* w, const int32_t* pos, int64_t T, int64_t k,
+             int64_t H, int dtype, void* out, bool weighted) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  const int rc = check_rows(h, T, k, H, dtype);
+  if (rc != PGEMM_OK) return rc;
+  if (T == 0 || H == 0) return PGEMM_OK;
+  if (!rows || !pos || !out || (weighted && !w)) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  if (ld < 0) return fail(h, PGEMM_ERR_INVALID_ARG, "row stride %lld", (long long)ld);
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  moe::SumArgs a;
+  a.rows = static_cast<const uint16_t*>(rows);
+  a.ld = ld;
+  a.w = w;
+  a.pos = pos;
+  a.out = static_cast<uint16_t*>(out);
+  a.T = (int)T;
+  a.k = (int)k;
+  a.H = (int)H;
+  a.n = (int)(T * k);
+  const bool al = H % 8 == 0 && ld % 8 == 0 && aligned16(rows) && aligned16(out);
+  if (weighted) launch_sum<true>(h, a, dtype, al);
+  else launch_sum<false>(h, a, dtype, al);
+  return launch_status(h, weighted ? "combine" : "dispatch backward");
+}
+
+} // namespace
+
+extern "C" {
+
+int pgemm_moe_dispatch_workspace(int64_t T, int64_t k, int64_t E, int64_t* bytes) {
+  if (!bytes || T < 0 || k < 1 || E < 1) return PGEMM_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (T > INT32_MAX || k > INT32_MAX || T * k > (int64_t)1 << 30 || E > moe::kMaxExperts) return PGEMM_ERR_UNSUPPORTED;
+  const int64_t n = T * k;
+  if (n > kSmallSlots) {
+    const int64_t chunk = sort_chunk(n);
+    *bytes = (n + chunk - 1) / chunk * (E + 1) * (int64_t)sizeof(int);
+  }
+  return PGEMM_OK;
+}
+
+int pgemm_moe_dispatch(pgemm_handle_t h, const void* x, int64_t ldx, const void* ids, int ids_type, int64_t T, int64_t k,
+                       int64_t E, int64_t H, int dtype, int32_t* offsets, int32_t* order, int32_t* pos, void* xs,
+                       void* work, int64_t work_bytes) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  int rc = check_rows(h, T, k, H, dtype);
+  if (rc == PGEMM_OK) rc = check_experts(h, E);
+  if (rc != PGEMM_OK) return rc;
+  if (ids_type != PGEMM_IDS_I32 && ids_type != PGEMM_IDS_I64)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "unknown ids type %d", ids_type);
+  if (ldx < 0) return fail(h, PGEMM_ERR_INVALID_ARG, "row stride %lld", (long long)ldx);
+  if (!offsets || (T > 0 && (!ids || !order || !pos || (H > 0 && (!x || !xs)))))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  int64_t need = 0;
+  rc = pgemm_moe_dispatch_workspace(T, k, E, &need);
+  if (rc != PGEMM_OK) return rc;
+  if (work_bytes < need || (need && !work))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "workspace of %lld bytes, %lld are needed", (long long)work_bytes,
+                (long long)need);
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  moe::SortArgs s;
+  s.ids = ids;
+  s.n = (int)(T * k);
+  s.E = (int)E;
+  s.chunk = (int)sort_chunk(T * k);
+  s.counts = static_cast<int*>(work);
+  s.offsets = offsets;
+  s.order = order;
+  s.pos = pos;
+  moe::MoveArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.xs = static_cast<uint16_t*>(xs);
+  a.pos = pos;
+  a.offsets = offsets;
+  a.T = (int)T;
+  a.k = (int)k;
+  a.E = (int)E;
+  a.H = (int)H;
+  a.n = s.n;
+  a.token_blocks = 0;
+  const bool al = H % 8 == 0 && ldx % 8 == 0 && aligned16(x) && aligned16(xs);
+  if (ids_type == PGEMM_IDS_I32) launch_dispatch<int32_t>(h, s, a, al);
+  else launch_dispatch<int64_t>(h, s, a, al);
+  return launch_status(h, "dispatch");
+}
+
+int pgemm_moe_dispatch_backward(pgemm_handle_t h, const void* dxs, int64_t lddxs, const int32_t* pos, int64_t T,
+                                int64_t k, int64_t H, int dtype, void* dx) {
+  return sum_impl(h, dxs, lddxs, nullptr, pos, T, k, H, dtype, dx, false);
+}
+
+int pgemm_moe_combine(pgemm_handle_t h, const void* ys, int64_t ldys, const float* w, const int32_t* pos, int64_t T,
+                      int64_t k, int64_t H, int dtype, void* out) {
+  return sum_impl(h, ys, ldys, w, pos, T, k, H, dtype, out, true);
+}
+
+int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
+                               const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
+                               int64_t E, int64_t H, int dtype, void* dys, float* dw) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  int rc = check_rows(h, T, k, H, dtype);
+  if (rc == PGEMM_OK) rc = check_experts(h, E);
+  if (rc != PGEMM_OK) return rc;
+  if (T == 0) return PGEMM_OK;
+  if (!w || !offsets || !pos || !dw || (H > 0 && (!dout || !ys || !dys)))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  if (lddout < 0 || ldys < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "row strides %lld, %lld", (long long)lddout, (long long)ldys);
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  moe::BackArgs a;
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.lddout = lddout;
+  a.ys = static_cast<const uint16_t*>(ys);
+  a.ldys = ldys;
+  a.w = w;
+  a.pos = pos;
+  a.offsets = offsets;
+  a.dys = static_cast<uint16_t*>(dys);
+  a.dw = dw;
+  a.T = (int)T;
+  a.k = (int)k;
+  a.E = (int)E;
+  a.H = (int)H;
+  a.n = (int)(T * k);
+  a.token_blocks = (int)token_blocks(T, H);
+  const bool al = H % 8 == 0 && lddout % 8 == 0 && ldys % 8 == 0 && aligned16(dout) && aligned16(ys) && aligned16(dys);
+  launch_back(h, a, dtype, al);
+  return launch_status(h, "combine backward");
+}
+
+} // extern "C"
