@@ -441,6 +441,37 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
                                const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
                                int64_t E, int64_t H, int dtype, void* dys, float* dw);
 
+/* ---- few rows times 4-bit weights -------------------------------------- */
+
+/* Format of the 4-bit codes. INT4: whole numbers 0..15 less a zero point;
+ * E2M1: sign, two exponent bits (bias 1), one mantissa bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives. */
+typedef enum { PGEMM_W4_INT4 = 0, PGEMM_W4_E2M1 = 1 } pgemm_w4_format_t;
+
+/* Enqueue y = x * dec(q)^T on the handle's stream, for the few rows of a
+ * decoding batch (any number is computed; each 64 read the weights again).
+ *   x: M rows of K elements, ldx apart (0 repeats one row); y: [M, N].
+ *   q: [E, N, ceil(K / 2)] bytes, code k of a row in byte k / 2, the even one
+ *     in the low nibble; a last half byte is ignored.
+ *   scales: [E, N, ceil(K / group)] of x's type, one for each `group` (32, 64
+ *     or 128) elements along K.
+ *   zeros: int4 zero points, uint8 of the same shape, their low four bits;
+ *     NULL: 8. E2M1 has none.
+ *   offsets: NULL: one matrix for all rows (E = 1); else E + 1 ascending row
+ *     bounds on the device, rows offsets[e]..offsets[e+1]-1 belonging to
+ *     matrix e; rows of none give zeros.
+ *   dtype: PGEMM_F16 or PGEMM_BF16, of x, scales and y.
+ * Each weight is (code - zero) * scale or e2m1(code) * scale, never rounded:
+ * the sum of a group is formed in fp32 from exact products, multiplied by its
+ * scale in fp32, and y is rounded once. K = 0 gives zeros. Nothing is
+ * allocated; pointers may have any alignment their elements have.
+ * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
+ * an unknown group, format or type, zeros with E2M1, or E > 1 without
+ * offsets; PGEMM_ERR_UNSUPPORTED for sizes above 2^30 or E above 65534. */
+int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, const void* scales, const void* zeros,
+                 const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int64_t E, int group, int fmt,
+                 int dtype);
+
 /* Benchmark aid, not part of the GEMM: make about `n_cus` CUs of device
  * `device` unavailable for about `microseconds`, asynchronously on the HIP
  * stream `hip_stream` (NULL = null stream). It launches n_cus workgroups

@@ -42,6 +42,9 @@ PGEMM_B_NK = 1
 PGEMM_IDS_I32 = 0
 PGEMM_IDS_I64 = 1
 
+PGEMM_W4_INT4 = 0
+PGEMM_W4_E2M1 = 1
+
 PGEMM_MAINLOOP_AUTO = 0
 PGEMM_MAINLOOP_LOCKSTEP = 1
 PGEMM_MAINLOOP_PINGPONG = 2
@@ -98,6 +101,7 @@ _moe_dispatch_backward = _sig("pgemm_moe_dispatch_backward", _int, _vp, _vp, _i6
 _moe_combine = _sig("pgemm_moe_combine", _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp)
 _moe_combine_backward = _sig("pgemm_moe_combine_backward", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
                              _i64, _i64, _int, _vp, _vp)
+_w4_run = _sig("pgemm_w4_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
 
@@ -301,6 +305,13 @@ def pgemm_moe_combine_backward(h, dout, lddout: int, ys, ldys: int, w, offsets, 
                                dtype: int, dys, dw) -> None:
     _check(_moe_combine_backward(h, _ptr(dout), lddout, _ptr(ys), ldys, _ptr(w), _ptr(offsets), _ptr(pos), T, k, E, H,
                                  dtype, _ptr(dys), _ptr(dw)), h)
+
+
+def pgemm_w4_run(h, x, ldx: int, q, scales, zeros, offsets, y, M: int, N: int, K: int, E: int, group: int, fmt: int,
+                 dtype: int) -> None:
+    """Enqueue y = x times 4-bit weights with group scales (pointers or tensors; zeros and offsets may be None)."""
+    _check(_w4_run(h, _ptr(x), ldx, _ptr(q), _ptr(scales), _ptr(zeros) or None, _ptr(offsets) or None, _ptr(y), M, N, K,
+                   E, group, fmt, dtype), h)
 
 
 _per_thread = threading.local()

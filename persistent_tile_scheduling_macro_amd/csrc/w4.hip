@@ -1,0 +1,73 @@
+// Entry point of the product with 4-bit weights.
+#include "context.h"
+#include "w4.h"
+
+using namespace pgemm;
+
+extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, const void* scales,
+                            const void* zeros, const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K,
+                            int64_t E, int group, int fmt, int dtype) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  if (M < 0 || N < 0 || K < 0 || E < 1 || ldx < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "sizes M=%lld N=%lld K=%lld E=%lld ldx=%lld", (long long)M, (long long)N,
+                (long long)K, (long long)E, (long long)ldx);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "group of %d, not 32, 64 or 128", group);
+  if (fmt != PGEMM_W4_INT4 && fmt != PGEMM_W4_E2M1) return fail(h, PGEMM_ERR_INVALID_ARG, "unknown 4-bit format %d", fmt);
+  if (dtype != PGEMM_F16 && dtype != PGEMM_BF16)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
+  if (zeros && fmt != PGEMM_W4_INT4) return fail(h, PGEMM_ERR_INVALID_ARG, "e2m1 weights have no zero points");
+  if (!offsets && E != 1) return fail(h, PGEMM_ERR_INVALID_ARG, "E=%lld experts without offsets", (long long)E);
+  constexpr int64_t lim = (int64_t)1 << 30;
+  if (M > lim || N > lim || K > lim) return fail(h, PGEMM_ERR_UNSUPPORTED, "sizes must not exceed 2^30");
+  if (E > 65534) return fail(h, PGEMM_ERR_UNSUPPORTED, "E=%lld experts, at most 65534", (long long)E);
+  if (M == 0 || N == 0) return PGEMM_OK;
+  if (!y || (K > 0 && (!x || !q || !scales))) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  if (K == 0) { // an empty sum
+    launch_fill_zero(y, M, N, N, h->stream);
+    return launch_status(h, "zero-fill");
+  }
+  w4::Args a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.q = static_cast<const uint8_t*>(q);
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.zeros = static_cast<const uint8_t*>(zeros);
+  a.offsets = offsets;
+  a.y = static_cast<uint16_t*>(y);
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.E = (int)E;
+  a.row_bytes = (int)((K + 1) / 2);
+  a.groups = (int)((K + group - 1) / group);
+  // Rows a workgroup takes at once: all of them up to 64. An expert's rows are known only on the
+  // device; twice the mean covers most experts in one pass, and a longer one loops.
+  const int64_t rows = offsets ? (2 * M + E - 1) / E : M;
+  const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  // Columns a wave takes: more share the reads of x, fewer fill the chip.
+  const int64_t experts = offsets ? (E < M ? E : M) : 1;
+  int cb = mb == 4 ? 2 : 4;
+  while (cb > 1 && experts * ((N + 16 * cb - 1) / (16 * cb)) < 2 * h->cus) cb /= 2;
+  const int64_t row_groups = offsets ? E + 1 : (M + 16 * mb - 1) / (16 * mb);
+  const int64_t cols = (N + 16 * cb - 1) / (16 * cb);
+  const int form = zeros ? w4::kInt4Zero : fmt == PGEMM_W4_E2M1 ? w4::kE2M1 : w4::kInt4;
+  const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, mb, cb) : w4::pick_bf16(form, group, mb, cb);
+  if (row_groups <= 65535) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::kWaves * 64), 0, h->stream, a);
+    return launch_status(h, "w4");
+  }
+  // more rows than one grid has: launches of at most 65535 row groups each
+  for (int64_t r = 0; r < row_groups; r += 65535) {
+    w4::Args b = a;
+    const int64_t from = r * 16 * mb, count = row_groups - r < 65535 ? row_groups - r : 65535;
+    b.x = a.x + from * ldx;
+    b.y = a.y + from * N;
+    b.M = (int)(M - from < count * 16 * mb ? M - from : count * 16 * mb);
+    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)count), dim3(w4::kWaves * 64), 0, h->stream, b);
+  }
+  return launch_status(h, "w4");
+}
