@@ -441,6 +441,33 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
                                const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
                                int64_t E, int64_t H, int dtype, void* dys, float* dw);
 
+/* ---- products of rows sorted by expert ---------------------------------- */
+/*
+ * offsets: E + 1 ascending row bounds on the device (those of
+ * pgemm_moe_dispatch), rows offsets[e]..offsets[e+1]-1 belonging to expert e.
+ * The host never reads them, so a call can be captured and replayed with
+ * other bounds. dtype is PGEMM_F16 or PGEMM_BF16; ld* is the distance of two
+ * rows in elements (0 repeats one row), w and the outputs are contiguous.
+ * Sums are fp32, rounded once, and the same on every run. Sizes and addresses
+ * may be odd; K and N of a multiple of 8 elements with rows at 16-byte
+ * addresses are the fastest. Nothing is allocated.
+ * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
+ * E < 1, an unknown layout or type; PGEMM_ERR_UNSUPPORTED for sizes above
+ * 2^30, E above 1024 or 2^31 output tiles. */
+
+/* Enqueue y[r] = x[r] * w[e(r)]. x: R rows of K; w: [E, K, N] for PGEMM_B_KN,
+ * [E, N, K] for PGEMM_B_NK; y: [R, N], zeros in rows of no expert (whatever x
+ * holds there) and for K = 0. The gradient of x is the same call on y's
+ * gradient with K and N exchanged and the other layout. */
+int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* w, const int32_t* offsets, void* y,
+                      int64_t R, int64_t E, int64_t K, int64_t N, int layout, int dtype);
+
+/* Enqueue c[e] = sum over the rows r of expert e of a[r]^T * b[r], zeros for
+ * an expert without rows. a: R rows of I; b: R rows of J; c: [E, I, J]. The
+ * gradient of w: (a, b) = (x, dy) for PGEMM_B_KN, (dy, x) for PGEMM_B_NK. */
+int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a, int64_t lda, const void* b, int64_t ldb,
+                              const int32_t* offsets, void* c, int64_t R, int64_t E, int64_t I, int64_t J, int dtype);
+
 /* ---- few rows times 4-bit weights -------------------------------------- */
 
 /* Format of the 4-bit codes. INT4: whole numbers 0..15 less a zero point;

@@ -101,6 +101,9 @@ _moe_dispatch_backward = _sig("pgemm_moe_dispatch_backward", _int, _vp, _vp, _i6
 _moe_combine = _sig("pgemm_moe_combine", _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp)
 _moe_combine_backward = _sig("pgemm_moe_combine_backward", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
                              _i64, _i64, _int, _vp, _vp)
+_grouped_run = _sig("pgemm_grouped_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int)
+_grouped_weight_grad = _sig("pgemm_grouped_weight_grad", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
+                            _i64, _int)
 _w4_run = _sig("pgemm_w4_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
@@ -307,6 +310,17 @@ def pgemm_moe_combine_backward(h, dout, lddout: int, ys, ldys: int, w, offsets, 
                                  dtype, _ptr(dys), _ptr(dw)), h)
 
 
+def pgemm_grouped_run(h, x, ldx: int, w, offsets, y, R: int, E: int, K: int, N: int, layout: int, dtype: int) -> None:
+    """Enqueue y[r] = x[r] @ w[expert of r] for rows sorted by expert (pointers or tensors)."""
+    _check(_grouped_run(h, _ptr(x), ldx, _ptr(w), _ptr(offsets), _ptr(y), R, E, K, N, layout, dtype), h)
+
+
+def pgemm_grouped_weight_grad(h, a, lda: int, b, ldb: int, offsets, c, R: int, E: int, I: int, J: int,
+                              dtype: int) -> None:
+    """Enqueue c[e] = a_e^T @ b_e over the rows of each expert."""
+    _check(_grouped_weight_grad(h, _ptr(a), lda, _ptr(b), ldb, _ptr(offsets), _ptr(c), R, E, I, J, dtype), h)
+
+
 def pgemm_w4_run(h, x, ldx: int, q, scales, zeros, offsets, y, M: int, N: int, K: int, E: int, group: int, fmt: int,
                  dtype: int) -> None:
     """Enqueue y = x times 4-bit weights with group scales (pointers or tensors; zeros and offsets may be None)."""
@@ -320,7 +334,7 @@ _per_thread = threading.local()
 def thread_handle(device):
     """The calling thread's own handle on a torch device, bound to torch's current stream there.
 
-    The operators of ``moe`` and ``w4`` use it when they are given none. It is created at the thread's first
+    The operators of ``moe`` and ``w4`` use it. It is created at the thread's first
     such call on the device, which therefore must not be made under graph capture, and lives as long as the process.
     """
     import torch

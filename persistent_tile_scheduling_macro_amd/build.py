@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "libpgemm.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["pgemm.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f8.hip", "kernels_pp_f16.hip",
            "kernels_pp_bf16.hip", "kernels_pp_f8.hip", "kernels_pw_f16.hip", "kernels_pw_bf16.hip", "kernels_pw_f8.hip",
-           "hold.hip", "moe.hip", "w4.hip", "w4_f16.hip",
+           "hold.hip", "moe.hip", "grouped.hip", "grouped_f16.hip", "grouped_bf16.hip", "w4.hip", "w4_f16.hip",
            "w4_bf16.hip"]
 ARCH = os.environ.get("PGEMM_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

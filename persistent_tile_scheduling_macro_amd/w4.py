@@ -1,7 +1,7 @@
 """Few rows times 4-bit weights with group scales: the product of a decoding step, dense or per expert.
 
 ``matmul`` checks shapes and types, makes the output and hands pointers to ``pgemm_w4_run``; it enqueues on torch's
-current stream (or, given ``handle``, on that handle's) and returns without waiting.
+current stream and returns without waiting.
 """
 from __future__ import annotations
 
@@ -14,7 +14,7 @@ _DTYPES = {torch.float16: PGEMM_F16, torch.bfloat16: PGEMM_BF16}
 _FORMATS = {"int4": PGEMM_W4_INT4, "e2m1": PGEMM_W4_E2M1}
 
 
-def matmul(x, q, scales, zeros=None, *, group: int, fmt: str = "int4", offsets=None, handle=None):
+def matmul(x, q, scales, zeros=None, *, group: int, fmt: str = "int4", offsets=None):
     """y [M, N] = x [M, K] times the transposed 4-bit weights.
 
     q uint8 [N, ceil(K/2)], code k of a row in byte k // 2, the even one in the low nibble; scales of x's type
@@ -63,7 +63,6 @@ def matmul(x, q, scales, zeros=None, *, group: int, fmt: str = "int4", offsets=N
         tensors.append(offsets)
     dev = _on_device("w4.matmul", *tensors)
     q, scales = q.contiguous(), scales.contiguous()
-    h = thread_handle(dev) if handle is None else handle
     y = torch.empty((M, N), dtype=x.dtype, device=dev)
-    pgemm_w4_run(h, x, ldx, q, scales, zeros, offsets, y, M, N, K, E, group, _FORMATS[fmt], _DTYPES[x.dtype])
+    pgemm_w4_run(thread_handle(dev), x, ldx, q, scales, zeros, offsets, y, M, N, K, E, group, _FORMATS[fmt], _DTYPES[x.dtype])
     return y
