@@ -269,14 +269,10 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   }
 }
 
+enum Body : int { kAnyAlignment = 0, kPingPong = 1 };
 typedef void (*kernel_fn)(Args);
-kernel_fn pick_f16(bool grad, bool nk);
-kernel_fn pick_bf16(bool grad, bool nk);
-
-template <int DT>
-kernel_fn pick(bool grad, bool nk) {
-  return grad ? grouped_kernel<DT, true, false> : nk ? grouped_kernel<DT, false, true> : grouped_kernel<DT, false, false>;
-}
+kernel_fn pick_f16(int body, bool grad, bool nk);
+kernel_fn pick_bf16(int body, bool grad, bool nk);
 
 } // namespace grouped
 } // namespace pgemm

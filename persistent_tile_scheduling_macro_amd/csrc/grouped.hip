@@ -20,14 +20,27 @@ int check(pgemm_ctx* h, int64_t R, int64_t E, int64_t K, int64_t N, int64_t lda,
   return PGEMM_OK;
 }
 
-int launch(pgemm_ctx* h, const grouped::Args& a, int64_t tiles, int dtype, bool grad, bool nk) {
-  if (tiles > INT32_MAX - 8) return fail(h, PGEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+
+// tile_rows(bm): upper bound of the tile rows of height bm over all experts.
+template <class F>
+int launch(pgemm_ctx* h, grouped::Args a, bool direct, int64_t mean_rows, F tile_rows, int dtype, bool grad, bool nk) {
+  const int body = direct && mean_rows >= 192 ? grouped::kPingPong : grouped::kAnyAlignment;
+  const int tile = body == grouped::kPingPong ? 256 : 128;
+  a.n_n = (a.N + tile - 1) / tile;
+  int64_t grid = tile_rows(tile) * a.n_n;
+  if (grid > INT32_MAX - 8) return fail(h, PGEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+  if (body == grouped::kPingPong) grid = grid < h->cus ? grid : h->cus; // persistent, one workgroup a CU
+  else if (!grad) grid = (grid + 7) / 8 * 8;
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
-  const grouped::kernel_fn kern = dtype == PGEMM_F16 ? grouped::pick_f16(grad, nk) : grouped::pick_bf16(grad, nk);
-  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(256), 0, h->stream, a);
+  const grouped::kernel_fn kern = dtype == PGEMM_F16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(body == grouped::kPingPong ? 512 : 256), 0, h->stream, a);
   return launch_status(h, "grouped product");
 }
+
+// Row strides up to which a tile's 32-bit offsets reach its last row (256 rows of 2-byte elements below 2^31).
+constexpr int64_t kMaxDirectStride = (int64_t)1 << 21;
 
 } // namespace
 
@@ -54,10 +67,10 @@ int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* 
   a.E = (int)E;
   a.K = (int)K;
   a.N = (int)N;
-  a.n_n = (int)((N + 127) / 128);
-  // every expert, and the rows of none, may leave one tile partly filled; a multiple of 8 for the XCDs
-  const int64_t tiles = ((R / 128 + E + 1) * a.n_n + 7) / 8 * 8;
-  return launch(h, a, tiles, dtype, false, layout == PGEMM_B_NK);
+  const bool direct = K % 8 == 0 && N % 8 == 0 && ldx % 8 == 0 && ldx <= kMaxDirectStride && a.ldb <= kMaxDirectStride &&
+                      aligned16(x) && aligned16(w) && aligned16(y);
+  // every expert, and the rows of none, may leave one tile partly filled
+  return launch(h, a, direct, R / E, [&](int bm) { return R / bm + E + 1; }, dtype, false, layout == PGEMM_B_NK);
 }
 
 int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda, const void* b_rows, int64_t ldb,
@@ -79,8 +92,9 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda,
   a.E = (int)E;
   a.M = (int)I;
   a.N = (int)J;
-  a.n_n = (int)((J + 127) / 128);
-  return launch(h, a, E * ((I + 127) / 128) * a.n_n, dtype, true, false);
+  const bool direct = I % 8 == 0 && J % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && lda <= kMaxDirectStride &&
+                      ldb <= kMaxDirectStride && aligned16(a_rows) && aligned16(b_rows) && aligned16(c);
+  return launch(h, a, direct, R / E, [&](int bm) { return E * ((I + bm - 1) / bm); }, dtype, true, false);
 }
 
 } // extern "C"

@@ -1,4 +1,4 @@
 // Instantiations of the grouped products for one element type.
-#include "grouped.h"
+#include "grouped_pp.h"
 
-pgemm::grouped::kernel_fn pgemm::grouped::pick_f16(bool grad, bool nk) { return pick<kF16>(grad, nk); }
+pgemm::grouped::kernel_fn pgemm::grouped::pick_f16(int body, bool grad, bool nk) { return pick<kF16>(body, grad, nk); }
