@@ -269,7 +269,9 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   }
 }
 
-enum Body : int { kAnyAlignment = 0, kPingPong = 1 };
+// Bodies: this file's, grouped_pp.h's, and grouped_few.h's (rows form) for
+// 16 or 32 rows at once, with one or two column blocks of N x K weights.
+enum Body : int { kAnyAlignment, kPingPong, kFew16, kFew16Wide, kFew32Wide };
 typedef void (*kernel_fn)(Args);
 kernel_fn pick_f16(int body, bool grad, bool nk);
 kernel_fn pick_bf16(int body, bool grad, bool nk);

@@ -22,20 +22,74 @@ int check(pgemm_ctx* h, int64_t R, int64_t E, int64_t K, int64_t N, int64_t lda,
 
 bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
 
+// Tile of a body: rows, columns, threads.
+struct Shape { int bm, bn, threads; };
+Shape shape_of(int body, bool nk) {
+  switch (body) {
+    case grouped::kPingPong: return {256, 256, 512};
+    case grouped::kFew16: return {16, nk ? 16 : 64, 512};
+    case grouped::kFew16Wide: return {16, nk ? 32 : 64, 512};
+    case grouped::kFew32Wide: return {32, nk ? 32 : 64, 512};
+    default: return {128, 128, 256};
+  }
+}
+
+// The body of the rows form. How many rows each expert has only the device
+// knows; with their mean, a body's time is estimated as rounds of workgroups
+// (so many of them run at once) times what one takes, or the time its reads
+// of the matrices take, if that is more:
+//   body     at once  a workgroup takes, us                     reads at
+//   few      512      4 + 0.0018 K (32 rows x 32 columns)       4.8 TB/s
+//   any      512      4 + 0.020 K; from 256 down 4 + 0.016 K    4 TB/s
+//   ping     256      4 + 0.0184 K                              4 TB/s
+// fitted to measured calls of K = 256 .. 4096, N = 64 .. 4096, 1 .. 64 experts
+// and 64 .. 16000 rows. Examples (few, any, ping-pong; us): one expert, 4096 x
+// 512, 256 rows 12, 61, 79, 4000 rows 62, 69, 80; eight experts, 1024 x 2048,
+// 1600 rows 46, 22, 27, 8000 rows 188, 62, 55; eight experts, 4096 x 4096,
+// 8000 rows 888, 400, 277.
+int pick_rows_body(const grouped::Args& a, bool direct, bool nk) {
+  const double experts = a.R < a.E ? a.R : a.E, mean = a.R / experts, K = a.K;
+  struct Cost { double groups, reads; };
+  auto cost = [&](int body) {
+    const Shape t = shape_of(body, nk);
+    double row_tiles = a.E == 1 ? __builtin_ceil(mean / t.bm) : mean / t.bm + 0.5; // an expert's last one is half full on average
+    if (row_tiles < 1) row_tiles = 1;
+    const bool few = t.bm < 128; // reads a matrix again for every row tile, the others find it in the L2
+    return Cost{experts * row_tiles * ((a.N + t.bn - 1) / t.bn), experts * (few ? row_tiles / 4.8e6 : 1 / 4.0e6) * K * a.N * 2};
+  };
+  auto longer = [](double x, double y) { return x > y ? x : y; };
+  int best = grouped::kAnyAlignment;
+  Cost c = cost(best);
+  const double crowd = c.groups < 256 ? 0 : c.groups > 512 ? 1 : c.groups / 256 - 1; // two on a CU
+  double least = longer(__builtin_ceil(c.groups / 512) * (4 + (0.016 + 0.004 * crowd) * K), c.reads);
+  if (direct) {
+    c = cost(grouped::kPingPong);
+    const double t = longer(__builtin_ceil(c.groups / 256) * (4 + 0.0184 * K), c.reads);
+    if (t < least) best = grouped::kPingPong, least = t;
+  }
+  if (K > 0 && (nk || a.N >= 4)) {
+    // 16 rows where they hold an expert's; two column blocks share the reads of x where that leaves enough workgroups
+    int body = grouped::kFew32Wide;
+    if (mean <= 8) body = cost(grouped::kFew16Wide).groups >= 512 ? grouped::kFew16Wide : grouped::kFew16;
+    c = cost(body);
+    if (longer(__builtin_ceil(c.groups / 512) * (4 + 0.0018 * K), c.reads) < least) best = body;
+  }
+  return best;
+}
+
 // tile_rows(bm): upper bound of the tile rows of height bm over all experts.
 template <class F>
-int launch(pgemm_ctx* h, grouped::Args a, bool direct, int64_t mean_rows, F tile_rows, int dtype, bool grad, bool nk) {
-  const int body = direct && mean_rows >= 192 ? grouped::kPingPong : grouped::kAnyAlignment;
-  const int tile = body == grouped::kPingPong ? 256 : 128;
-  a.n_n = (a.N + tile - 1) / tile;
-  int64_t grid = tile_rows(tile) * a.n_n;
+int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool grad, bool nk) {
+  const Shape t = shape_of(body, nk);
+  a.n_n = (a.N + t.bn - 1) / t.bn;
+  int64_t grid = tile_rows(t.bm) * a.n_n;
   if (grid > INT32_MAX - 8) return fail(h, PGEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
   if (body == grouped::kPingPong) grid = grid < h->cus ? grid : h->cus; // persistent, one workgroup a CU
   else if (!grad) grid = (grid + 7) / 8 * 8;
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
   const grouped::kernel_fn kern = dtype == PGEMM_F16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(body == grouped::kPingPong ? 512 : 256), 0, h->stream, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(t.threads), 0, h->stream, a);
   return launch_status(h, "grouped product");
 }
 
@@ -70,7 +124,8 @@ int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* 
   const bool direct = K % 8 == 0 && N % 8 == 0 && ldx % 8 == 0 && ldx <= kMaxDirectStride && a.ldb <= kMaxDirectStride &&
                       aligned16(x) && aligned16(w) && aligned16(y);
   // every expert, and the rows of none, may leave one tile partly filled
-  return launch(h, a, direct, R / E, [&](int bm) { return R / bm + E + 1; }, dtype, false, layout == PGEMM_B_NK);
+  const bool nk = layout == PGEMM_B_NK;
+  return launch(h, a, pick_rows_body(a, direct, nk), [&](int bm) { return R / bm + E + 1; }, dtype, false, nk);
 }
 
 int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda, const void* b_rows, int64_t ldb,
@@ -94,7 +149,8 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda,
   a.N = (int)J;
   const bool direct = I % 8 == 0 && J % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && lda <= kMaxDirectStride &&
                       ldb <= kMaxDirectStride && aligned16(a_rows) && aligned16(b_rows) && aligned16(c);
-  return launch(h, a, direct, R / E, [&](int bm) { return E * ((I + bm - 1) / bm); }, dtype, true, false);
+  const int body = direct && R / E >= 192 ? grouped::kPingPong : grouped::kAnyAlignment;
+  return launch(h, a, body, [&](int bm) { return E * ((I + bm - 1) / bm); }, dtype, true, false);
 }
 
 } // extern "C"

@@ -1,4 +1,4 @@
 // Instantiations of the grouped products for one element type.
-#include "grouped_pp.h"
+#include "grouped_impl.h"
 
 pgemm::grouped::kernel_fn pgemm::grouped::pick_f16(int body, bool grad, bool nk) { return pick<kF16>(body, grad, nk); }

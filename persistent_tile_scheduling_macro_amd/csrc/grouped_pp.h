@@ -315,12 +315,5 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
     run(I1{});
 }
 
-template <int DT>
-kernel_fn pick(int body, bool grad, bool nk) {
-  if (body == kPingPong)
-    return grad ? grouped_pp_kernel<DT, true, false> : nk ? grouped_pp_kernel<DT, false, true> : grouped_pp_kernel<DT, false, false>;
-  return grad ? grouped_kernel<DT, true, false> : nk ? grouped_kernel<DT, false, true> : grouped_kernel<DT, false, false>;
-}
-
 } // namespace grouped
 } // namespace pgemm
