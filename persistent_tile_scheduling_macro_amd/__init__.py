@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpgemm.so")
@@ -326,34 +325,6 @@ def pgemm_w4_run(h, x, ldx: int, q, scales, zeros, offsets, y, M: int, N: int, K
     """Enqueue y = x times 4-bit weights with group scales (pointers or tensors; zeros and offsets may be None)."""
     _check(_w4_run(h, _ptr(x), ldx, _ptr(q), _ptr(scales), _ptr(zeros) or None, _ptr(offsets) or None, _ptr(y), M, N, K,
                    E, group, fmt, dtype), h)
-
-
-_per_thread = threading.local()
-
-
-def thread_handle(device):
-    """The calling thread's own handle on a torch device, bound to torch's current stream there.
-
-    The operators of ``moe`` and ``w4`` use it. It is created at the thread's first
-    such call on the device, which therefore must not be made under graph capture, and lives as long as the process.
-    """
-    import torch
-
-    index = device.index
-    if index is None:
-        index = torch.cuda.current_device()
-    handles = getattr(_per_thread, "handles", None)
-    if handles is None:
-        handles = _per_thread.handles = {}
-    h = handles.get(index)
-    if h is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("call the operator once outside graph capture first: its handle is created then")
-        before = torch.cuda.current_device()
-        h = handles[index] = pgemm_create(index)
-        torch.cuda.set_device(before)  # pgemm_create makes its device current
-    _check(_set_stream(h, torch.cuda.current_stream(index).cuda_stream), h)
-    return h
 
 
 def matmul(A, B, C=None, *, sched: str | int = "static", grid_multiple: int = 0, handle=None):

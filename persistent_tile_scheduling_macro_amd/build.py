@@ -1,4 +1,5 @@
-"""Build libpgemm.so (the HIP kernels and the C-ABI host code) for gfx950.
+"""Build libpgemm.so (the HIP kernels and the C-ABI host code) for gfx950, and
+_ops.so, the torch binding of the operators (host code, linked to it).
 
 Each translation unit is compiled in parallel with hipcc, then linked into
 one shared library next to this file. Run as ``python -m
@@ -14,15 +15,18 @@ a memory round trip per step.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpgemm.so")
+OPS = os.path.join(HERE, "_ops.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["pgemm.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f8.hip", "kernels_pp_f16.hip",
            "kernels_pp_bf16.hip", "kernels_pp_f8.hip", "kernels_pw_f16.hip", "kernels_pw_bf16.hip", "kernels_pw_f8.hip",
@@ -72,6 +76,20 @@ def _compile(src: str):
     return obj, parse_resource_remarks(r.stderr)
 
 
+def _build_ops(tmp: str) -> None:
+    """Compile the binding against torch's headers and the library just linked."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
+           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
+           "-L" + HERE, "-lpgemm", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the torch binding failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
@@ -93,8 +111,10 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_ops(OPS + ".tmp")
+    os.replace(OPS + ".tmp", OPS)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {OPS}")
     return LIB
 
 
