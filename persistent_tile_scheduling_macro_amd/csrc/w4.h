@@ -3,13 +3,17 @@
 //   dec = e2m1(code) * s[n][k / group]                 (sign, two exponent bits, one mantissa bit)
 // Codes lie along K, two to a byte, the lower nibble first.
 //
-// The codes' bytes bound it: each is read once and used for every row of x.
-// A wave owns CB blocks of 16 columns and a range of K; lane (g, s), s < 16,
-// loads 16 bytes (32 codes) of column s at a time, so the four lanes of a
-// column read 64 bytes in a row, straight into registers: no weight is used
-// by two waves, so LDS would only add a copy. Two swaps between lane groups
-// then give lane group g the codes 8g..8g+7 of each 32, the operand layout of
-// the 16x16x32 MFMA, whose 32 products all lie in one scale group.
+// The codes' bytes bound it: each is read once and used for up to 32 rows of
+// x. A wave owns CB blocks of 16 columns and a range of K, 128 k a step. The
+// MFMA wants column s in lane (g, s), but loads in that layout make every
+// lane a request of its own (consecutive lanes lie a row apart), and the
+// address unit then bounds it (16 x 16384 x 8192: 41 us). So loads of codes,
+// x and scales run along the rows, and each wave turns them in its own LDS:
+//   codes   four lanes read 64 bytes of a column; lane (g, s) takes the four
+//           bytes 16 i + 4 g of column s for sub-step i, 32 k in one MFMA, all
+//           in one scale group;
+//   x       16 lanes read 256 bytes of a row; operands of 16 bytes;
+//   scales, zero points   read for 32 groups at a time.
 //
 // Codes become operands without rounding: code - z is a whole number up to
 // 15 and an e2m1 value has two significant bits, so both are exact in either
@@ -20,7 +24,7 @@
 // few) and their sums are joined in LDS in a fixed order.
 #pragma once
 
-#include "device_common.h"
+#include "moe_rows.h"
 
 namespace pgemm {
 namespace w4 {
@@ -31,8 +35,6 @@ constexpr int kWaves = 8;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
@@ -127,15 +129,20 @@ __device__ inline float scale_value(uint16_t b) {
   else return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
-template <int DT, int FMT, int GROUP, int MB, int CB>
-__global__ void __launch_bounds__(kWaves * 64) w4_kernel(Args a) {
-  constexpr int GPS = kStep / GROUP; // scale groups of a step
-  constexpr int SPG = GROUP / 32;    // MFMA k-groups of a scale group
-  constexpr int SR = (GPS + 1) / 2;  // registers that hold a step's scales
-  constexpr int XD = MB == 1 ? 4 : MB == 2 ? 2 : 1; // 32-k pieces of x read ahead
+// ROWS: rows of x taken at once, 4, 16 or 32 (4 reads only those; the MFMA always has 16).
+template <int DT, int FMT, int GROUP, int ROWS, int CB>
+__global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Args a) {
+  constexpr int MB = (ROWS + 15) / 16, XL = ROWS / 4; // row blocks; loads of x a step
+  constexpr int GPS = kStep / GROUP;                  // scale groups of a step
+  constexpr int SPG = GROUP / 32;                     // MFMA k-groups of a scale group
+  constexpr int GC = 32, CHUNK = GC / GPS;            // scale groups kept at a time, their steps
+  constexpr int D = 2;                                // steps in flight
+  constexpr int SROW = 2 * GC + 4, ZROW = GC + 4;     // LDS rows of scales and zero points, off the banks' period
+  constexpr int XB = ROWS * 256, WB = CB * 1024, SB = CB * 16 * SROW, ZB = FMT == kInt4Zero ? CB * 16 * ZROW : 0;
+  constexpr int TURN = (XB + WB + SB + ZB + 15) / 16 * 16, JOIN = CB * MB * 1024;
   typedef typename Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;
-  __shared__ floatx4_t red[kWaves][CB * MB * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * (TURN > JOIN ? TURN : JOIN)];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, s = lane & 15;
@@ -154,167 +161,176 @@ __global__ void __launch_bounds__(kWaves * 64) w4_kernel(Args a) {
     m0 = min(max(a.offsets[e], 0), a.M);
     m1 = min(max(a.offsets[e + 1], m0), a.M);
   } else {
-    m0 = blockIdx.y * 16 * MB;
-    m1 = min(m0 + 16 * MB, a.M);
+    m0 = blockIdx.y * ROWS;
+    m1 = min(m0 + ROWS, a.M);
   }
   if (m0 >= m1) return;
 
-  const uint8_t* wrow[CB];
-  const uint16_t* srow[CB];
-  const uint8_t* zrow[CB];
+  uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + XB, *turn_s = turn_w + WB, *turn_z = turn_s + SB;
+  // a load's lanes: four to a column (codes, scales), 16 to a row of x
+  const int wcol = lane >> 2, wpart = lane & 3, xr = lane >> 4, xpart = lane & 15;
+  const uint8_t* wp[CB];
+  auto column = [&](int c) __attribute__((always_inline)) { // columns past N read the last one and are not stored
+    return (int64_t)e * a.N + min(n0 + 16 * c + wcol, a.N - 1);
+  };
 #pragma unroll
-  for (int c = 0; c < CB; ++c) {
-    const int n = min(n0 + 16 * c + s, a.N - 1); // columns past N read the last one and are not stored
-    const int64_t col = (int64_t)e * a.N + n;
-    wrow[c] = a.q + col * a.row_bytes + 16 * g;
-    srow[c] = a.scales + col * a.groups;
-    zrow[c] = FMT == kInt4Zero ? a.zeros + col * a.groups : nullptr;
-  }
-  // the waves share the whole steps of K evenly; the last wave also takes the partial one
+  for (int c = 0; c < CB; ++c) wp[c] = a.q + column(c) * a.row_bytes + 16 * wpart;
+  // the waves share the whole steps of K evenly; the 32-k pieces behind them go to one wave each
   const int whole = a.K / kStep;
   const int first = (int)((int64_t)wave * whole / kWaves), last = (int)((int64_t)(wave + 1) * whole / kWaves);
-  const bool tail = wave == kWaves - 1 && whole * kStep < a.K;
 
-  for (; m0 < m1; m0 += 16 * MB) {
+  auto wave_fence = [&]() __attribute__((always_inline)) { // LDS serves a wave in order: only the compiler has to be held
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+
+  for (; m0 < m1; m0 += ROWS) {
     floatx4_t acc[MB][CB], d[MB][CB];
-    const uint16_t* xrow[MB];
-#pragma unroll
-    for (int b = 0; b < MB; ++b) { // rows past the last read the last one and are not stored
-      xrow[b] = a.x + (int64_t)min(m0 + 16 * b + s, m1 - 1) * a.ldx + 8 * g;
-#pragma unroll
-      for (int c = 0; c < CB; ++c) acc[b][c] = d[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    }
-
-    struct Step { // what one step reads of the weights
-      u32x4 w[CB];
-      uint32_t sc[CB][SR], z[CB];
-    };
-    auto load = [&](Step& t, int step) __attribute__((always_inline)) {
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        t.w[c] = *reinterpret_cast<const u32x4_any*>(wrow[c] + (int64_t)step * (kStep / 2));
-        __builtin_memcpy(t.sc[c], srow[c] + (int64_t)step * GPS, 2 * GPS);
-        if constexpr (FMT == kInt4Zero) __builtin_memcpy(&t.z[c], zrow[c] + (int64_t)step * GPS, GPS);
-      }
-    };
-    // 32 k of x, k0 = 32 * sub
-    auto load_x = [&](u32x4 (&x)[MB], int sub) __attribute__((always_inline)) {
-#pragma unroll
-      for (int b = 0; b < MB; ++b) x[b] = *reinterpret_cast<const u32x4_any*>(xrow[b] + (int64_t)sub * 32);
-    };
-    // 4 x 4 transpose of a step's registers over the lane groups
-    auto transpose = [&](Step& t) __attribute__((always_inline)) {
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        auto r = __builtin_amdgcn_permlane32_swap(t.w[c][0], t.w[c][2], false, false);
-        auto u = __builtin_amdgcn_permlane32_swap(t.w[c][1], t.w[c][3], false, false);
-        auto lo = __builtin_amdgcn_permlane16_swap(r[0], u[0], false, false);
-        auto hi = __builtin_amdgcn_permlane16_swap(r[1], u[1], false, false);
-        t.w[c] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-      }
-    };
-    // sub-step I of a step: 32 k of every block; a scale group's last one adds its sum to acc
-    auto sub_step = [&](Step& t, u32x4 (&x)[MB], auto ic) __attribute__((always_inline)) {
-      constexpr int I = decltype(ic)::value, P = I / SPG;
-      frag_t xo[MB];
-#pragma unroll
-      for (int b = 0; b < MB; ++b) xo[b] = __builtin_bit_cast(frag_t, order_x<DT, FMT>(x[b]));
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        const uint32_t zz = zero_operand<DT, FMT>(FMT == kInt4Zero ? (t.z[c] >> (8 * P)) & 15u : 8u);
-        const frag_t w = __builtin_bit_cast(frag_t, decode<DT, FMT>(t.w[c][I], zz));
-#pragma unroll
-        for (int b = 0; b < MB; ++b) d[b][c] = mfma(xo[b], w, I % SPG ? d[b][c] : floatx4_t{0.f, 0.f, 0.f, 0.f});
-        if constexpr (I % SPG == SPG - 1) {
-          const float sc = scale_value<DT>((uint16_t)(t.sc[c][P / 2] >> (16 * (P & 1))));
-#pragma unroll
-          for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[b][c][r] = __builtin_fmaf(sc, d[b][c][r], acc[b][c][r]);
-        }
-      }
-    };
-    typedef std::integral_constant<int, 0> I0;
-    typedef std::integral_constant<int, 1> I1;
-    typedef std::integral_constant<int, 2> I2;
-    typedef std::integral_constant<int, 3> I3;
-
-    if (first < last) {
-      u32x4 x[XD][MB]; // the next XD sub-steps of x
-      const int last_sub = 4 * last - 1;
-#pragma unroll
-      for (int i = 0; i < XD; ++i) load_x(x[i], 4 * first + i);
-      auto compute = [&](Step& t, int step) __attribute__((always_inline)) {
-        transpose(t);
-        auto sub = [&](auto ic) __attribute__((always_inline)) {
-          constexpr int I = decltype(ic)::value;
-          sub_step(t, x[I % XD], ic);
-          // past the range the last one is read again, and not used
-          load_x(x[I % XD], min(4 * step + I + XD, last_sub));
-          __builtin_amdgcn_sched_barrier(0); // one sub-step's operands live at a time
-        };
-        sub(I0{});
-        sub(I1{});
-        sub(I2{});
-        sub(I3{});
-      };
-      Step p, q;
-      load(p, first);
-      int t = first;
-      for (; t + 1 < last; t += 2) {
-        load(q, t + 1);
-        compute(p, t);
-        load(p, min(t + 2, last - 1));
-        compute(q, t + 1);
-      }
-      if (t < last) compute(p, t);
-    }
-    if (tail) {
-      // 32 k at a time, each lane its own four bytes and eight elements: nothing past a row's end
-      // is read, and codes past K meet zeros of x
-#pragma unroll 1
-      for (int sub = 4 * whole; sub * 32 < a.K; ++sub) {
-        const int xn = a.K - 32 * sub - 8 * g, wn = a.row_bytes - 16 * sub - 4 * g;
-        u32x4 x[MB];
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t v = 0;
-            if (2 * j < xn) v = xrow[b][32 * sub + 2 * j];
-            if (2 * j + 1 < xn) v |= (uint32_t)xrow[b][32 * sub + 2 * j + 1] << 16;
-            x[b][j] = v;
-          }
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          const uint8_t* w = wrow[c] - 16 * g + 16 * sub + 4 * g;
-          uint32_t v = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < wn) v |= (uint32_t)w[j] << (8 * j);
-          uint32_t z = 8;
-          if constexpr (FMT == kInt4Zero) z = zrow[c][sub / SPG] & 15u;
-          const frag_t wf = __builtin_bit_cast(frag_t, decode<DT, FMT>(v, zero_operand<DT, FMT>(z)));
-          const float sc = scale_value<DT>(srow[c][sub / SPG]);
-#pragma unroll
-          for (int b = 0; b < MB; ++b) {
-            const floatx4_t one = mfma(__builtin_bit_cast(frag_t, order_x<DT, FMT>(x[b])), wf, floatx4_t{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[b][c][r] = __builtin_fmaf(sc, one[r], acc[b][c][r]);
-          }
-        }
-      }
-    }
-
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int c = 0; c < CB; ++c) red[wave][(c * MB + b) * 64 + lane] = acc[b][c];
+      for (int c = 0; c < CB; ++c) acc[b][c] = d[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    const uint16_t* xp[XL];
+#pragma unroll
+    for (int i = 0; i < XL; ++i) // rows past the last read the last one and are not stored
+      xp[i] = a.x + min(m0 + 4 * i + xr, m1 - 1) * a.ldx + 8 * xpart;
+
+    struct Step { // what one step reads
+      u32x4 w[CB], x[XL];
+    };
+    auto load = [&](Step& t, int step) __attribute__((always_inline)) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) t.w[c] = *reinterpret_cast<const u32x4_any*>(wp[c] + (int64_t)step * (kStep / 2));
+#pragma unroll
+      for (int i = 0; i < XL; ++i) t.x[i] = *reinterpret_cast<const u32x4_any*>(xp[i] + (int64_t)step * kStep);
+    };
+    // scales and zero points of the GC groups from step's first on
+    auto refill = [&](int step) __attribute__((always_inline)) {
+      const int g0 = step * GPS + 8 * wpart, left = a.groups - g0;
+#pragma unroll 1 // not in a hurry, and its registers are needed elsewhere
+      for (int c = 0; c < CB; ++c) {
+        const uint16_t* sp = a.scales + column(c) * a.groups + g0;
+        u32x4 v = {0, 0, 0, 0};
+        if (left >= 8) v = *reinterpret_cast<const u32x4_any*>(sp);
+        else if (left > 0) v = moe::load_part(sp, left);
+        uint32_t* at = reinterpret_cast<uint32_t*>(turn_s + (16 * c + wcol) * SROW + 16 * wpart);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at[j] = v[j];
+        if constexpr (FMT == kInt4Zero) {
+          const uint8_t* zp = a.zeros + column(c) * a.groups + g0;
+          uint32_t z[2] = {0, 0};
+          if (left >= 8) {
+            __builtin_memcpy(z, zp, 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < left) z[j >> 2] |= (uint32_t)zp[j] << (8 * (j & 3));
+          }
+          uint32_t* to = reinterpret_cast<uint32_t*>(turn_z + (16 * c + wcol) * ZROW + 8 * wpart);
+          to[0] = z[0];
+          to[1] = z[1];
+        }
+      }
+    };
+    auto compute = [&](Step& t, int step) __attribute__((always_inline)) {
+      wave_fence(); // the last step's reads come first
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        const int r = 4 * i + xr;
+        *reinterpret_cast<u32x4*>(turn_x + r * 256 + 16 * (xpart ^ (2 * (r & 7)))) = t.x[i];
+      }
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+        *reinterpret_cast<u32x4*>(turn_w + c * 1024 + wcol * 64 + 16 * (wpart ^ (wcol >> 2))) = t.w[c];
+      if ((step - first) % CHUNK == 0) refill(step);
+      wave_fence();
+      const int gr = (step - first) % CHUNK * GPS;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        frag_t xo[MB];
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          const int r = ROWS == 4 ? s & 3 : 16 * b + s;
+          xo[b] = __builtin_bit_cast(
+              frag_t, order_x<DT, FMT>(*reinterpret_cast<const u32x4*>(turn_x + r * 256 + 16 * ((4 * i + g) ^ (2 * (r & 7))))));
+        }
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          const int p = gr + i / SPG;
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(turn_w + c * 1024 + s * 64 + 16 * (i ^ (s >> 2)) + 4 * g);
+          const uint32_t zz = zero_operand<DT, FMT>(FMT == kInt4Zero ? turn_z[(16 * c + s) * ZROW + p] & 15u : 8u);
+          const frag_t w = __builtin_bit_cast(frag_t, decode<DT, FMT>(v, zz));
+#pragma unroll
+          for (int b = 0; b < MB; ++b) d[b][c] = mfma(xo[b], w, i % SPG ? d[b][c] : floatx4_t{0.f, 0.f, 0.f, 0.f});
+          if (i % SPG == SPG - 1) { // a scale group is complete
+            const float sc = scale_value<DT>(*reinterpret_cast<const uint16_t*>(turn_s + (16 * c + s) * SROW + 2 * p));
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[b][c][r] = __builtin_fmaf(sc, d[b][c][r], acc[b][c][r]);
+          }
+        }
+      }
+    };
+
+    if (first < last) {
+      Step t[D];
+#pragma unroll
+      for (int j = 0; j < D; ++j) load(t[j], min(first + j, last - 1));
+      for (int i = first; i < last; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+          if (i + j < last) compute(t[j], i + j);
+          load(t[j], min(i + j + D, last - 1)); // past the range the last one again, not used
+        }
+      }
+    }
+    // each lane its own four bytes and eight elements of a piece: nothing past a row's end is read,
+    // and codes past K meet zeros of x
+    for (int sub = 4 * whole + kWaves - 1 - wave; sub * 32 < a.K; sub += kWaves) {
+      const int xn = a.K - 32 * sub - 8 * g, wn = a.row_bytes - 16 * sub - 4 * g;
+      u32x4 x[MB];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const uint16_t* xrow = a.x + min(m0 + 16 * b + s, m1 - 1) * a.ldx + 32 * sub + 8 * g;
+        x[b] = xn >= 8 ? *reinterpret_cast<const u32x4_any*>(xrow) : xn > 0 ? moe::load_part(xrow, xn) : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        const int64_t n = (int64_t)e * a.N + min(n0 + 16 * c + s, a.N - 1);
+        const uint8_t* w = a.q + n * a.row_bytes + 16 * sub + 4 * g;
+        uint32_t v = 0;
+        if (wn >= 4) {
+          __builtin_memcpy(&v, w, 4);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (j < wn) v |= (uint32_t)w[j] << (8 * j);
+        }
+        const int64_t at = n * a.groups + sub / SPG;
+        const uint32_t z = FMT == kInt4Zero ? a.zeros[at] & 15u : 8u;
+        const frag_t wf = __builtin_bit_cast(frag_t, decode<DT, FMT>(v, zero_operand<DT, FMT>(z)));
+        const float sc = scale_value<DT>(a.scales[at]);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          const floatx4_t one = mfma(__builtin_bit_cast(frag_t, order_x<DT, FMT>(x[b])), wf, floatx4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[b][c][r] = __builtin_fmaf(sc, one[r], acc[b][c][r]);
+        }
+      }
+    }
+
+    __syncthreads(); // every wave is through with its part of the LDS
+    floatx4_t* join = reinterpret_cast<floatx4_t*>(lds);
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int c = 0; c < CB; ++c) join[(wave * CB * MB + c * MB + b) * 64 + lane] = acc[b][c];
     __syncthreads();
     for (int i = tid; i < CB * MB * 64; i += kWaves * 64) {
-      floatx4_t v = red[0][i];
+      floatx4_t v = join[i];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += red[w][i];
+      for (int w = 1; w < kWaves; ++w) v += join[w * CB * MB * 64 + i];
       const int l = i & 63, b = (i >> 6) % MB, c = (i >> 6) / MB;
       const int n = n0 + 16 * c + (l & 15), m = m0 + 16 * b + 4 * (l >> 4);
 #pragma unroll
@@ -327,23 +343,27 @@ __global__ void __launch_bounds__(kWaves * 64) w4_kernel(Args a) {
 }
 
 typedef void (*kernel_fn)(Args);
-// The kernel for a format, group size, row blocks mb (1, 2 or 4) and column blocks cb (1, 2 or 4; up to 2 with mb = 4).
-kernel_fn pick_f16(int fmt, int group, int mb, int cb);
-kernel_fn pick_bf16(int fmt, int group, int mb, int cb);
+// The kernel for a format, group size, rows at once (4, 16 or 32) and column blocks (1 or 2).
+kernel_fn pick_f16(int fmt, int group, int rows, int cb);
+kernel_fn pick_bf16(int fmt, int group, int rows, int cb);
 
 template <int DT, int FMT, int GROUP>
-kernel_fn pick_shape(int mb, int cb) {
-  if (mb == 1) return cb == 1 ? w4_kernel<DT, FMT, GROUP, 1, 1> : cb == 2 ? w4_kernel<DT, FMT, GROUP, 1, 2> : w4_kernel<DT, FMT, GROUP, 1, 4>;
-  if (mb == 2) return cb == 1 ? w4_kernel<DT, FMT, GROUP, 2, 1> : cb == 2 ? w4_kernel<DT, FMT, GROUP, 2, 2> : w4_kernel<DT, FMT, GROUP, 2, 4>;
-  return cb == 1 ? w4_kernel<DT, FMT, GROUP, 4, 1> : w4_kernel<DT, FMT, GROUP, 4, 2>;
+kernel_fn pick_shape(int rows, int cb) {
+  if (rows == 4) return cb == 1 ? w4_kernel<DT, FMT, GROUP, 4, 1> : w4_kernel<DT, FMT, GROUP, 4, 2>;
+  if (rows == 16) return cb == 1 ? w4_kernel<DT, FMT, GROUP, 16, 1> : w4_kernel<DT, FMT, GROUP, 16, 2>;
+  return cb == 1 ? w4_kernel<DT, FMT, GROUP, 32, 1> : w4_kernel<DT, FMT, GROUP, 32, 2>;
 }
 template <int DT, int FMT>
-kernel_fn pick_group(int group, int mb, int cb) {
-  return group == 32 ? pick_shape<DT, FMT, 32>(mb, cb) : group == 64 ? pick_shape<DT, FMT, 64>(mb, cb) : pick_shape<DT, FMT, 128>(mb, cb);
+kernel_fn pick_group(int group, int rows, int cb) {
+  return group == 32   ? pick_shape<DT, FMT, 32>(rows, cb)
+         : group == 64 ? pick_shape<DT, FMT, 64>(rows, cb)
+                       : pick_shape<DT, FMT, 128>(rows, cb);
 }
 template <int DT>
-kernel_fn pick(int fmt, int group, int mb, int cb) {
-  return fmt == kInt4 ? pick_group<DT, kInt4>(group, mb, cb) : fmt == kInt4Zero ? pick_group<DT, kInt4Zero>(group, mb, cb) : pick_group<DT, kE2M1>(group, mb, cb);
+kernel_fn pick(int fmt, int group, int rows, int cb) {
+  return fmt == kInt4       ? pick_group<DT, kInt4>(group, rows, cb)
+         : fmt == kInt4Zero ? pick_group<DT, kInt4Zero>(group, rows, cb)
+                            : pick_group<DT, kE2M1>(group, rows, cb);
 }
 
 } // namespace w4

@@ -44,18 +44,17 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   a.E = (int)E;
   a.row_bytes = (int)((K + 1) / 2);
   a.groups = (int)((K + group - 1) / group);
-  // Rows a workgroup takes at once: all of them up to 64. An expert's rows are known only on the
-  // device; twice the mean covers most experts in one pass, and a longer one loops.
-  const int64_t rows = offsets ? (2 * M + E - 1) / E : M;
-  const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  // Columns a wave takes: more share the reads of x, fewer fill the chip.
+  // Rows a workgroup takes at once. An expert's rows are known only on the device: twice the mean
+  // covers most experts in one pass, and a longer one loops.
+  const int64_t mean = offsets ? (2 * M + E - 1) / E : M;
+  const int rows = mean <= 4 ? 4 : mean <= 16 ? 16 : 32;
+  // Columns a wave takes: two blocks share the reads of x, one where two would leave CUs idle.
   const int64_t experts = offsets ? (E < M ? E : M) : 1;
-  int cb = mb == 4 ? 2 : 4;
-  while (cb > 1 && experts * ((N + 16 * cb - 1) / (16 * cb)) < 2 * h->cus) cb /= 2;
-  const int64_t row_groups = offsets ? E + 1 : (M + 16 * mb - 1) / (16 * mb);
+  const int cb = experts * ((N + 31) / 32) >= 2 * h->cus ? 2 : 1;
+  const int64_t row_groups = offsets ? E + 1 : (M + rows - 1) / rows;
   const int64_t cols = (N + 16 * cb - 1) / (16 * cb);
   const int form = zeros ? w4::kInt4Zero : fmt == PGEMM_W4_E2M1 ? w4::kE2M1 : w4::kInt4;
-  const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, mb, cb) : w4::pick_bf16(form, group, mb, cb);
+  const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, rows, cb) : w4::pick_bf16(form, group, rows, cb);
   if (row_groups <= 65535) {
     hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::kWaves * 64), 0, h->stream, a);
     return launch_status(h, "w4");
@@ -63,10 +62,10 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   // more rows than one grid has: launches of at most 65535 row groups each
   for (int64_t r = 0; r < row_groups; r += 65535) {
     w4::Args b = a;
-    const int64_t from = r * 16 * mb, count = row_groups - r < 65535 ? row_groups - r : 65535;
+    const int64_t from = r * rows, count = row_groups - r < 65535 ? row_groups - r : 65535;
     b.x = a.x + from * ldx;
     b.y = a.y + from * N;
-    b.M = (int)(M - from < count * 16 * mb ? M - from : count * 16 * mb);
+    b.M = (int)(M - from < count * rows ? M - from : count * rows);
     hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)count), dim3(w4::kWaves * 64), 0, h->stream, b);
   }
   return launch_status(h, "w4");

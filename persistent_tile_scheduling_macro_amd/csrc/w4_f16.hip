@@ -1,4 +1,4 @@
 // Instantiations of the 4-bit product for one element type.
 #include "w4.h"
 
-pgemm::w4::kernel_fn pgemm::w4::pick_f16(int fmt, int group, int mb, int cb) { return pick<kF16>(fmt, group, mb, cb); }
+pgemm::w4::kernel_fn pgemm::w4::pick_f16(int fmt, int group, int rows, int cb) { return pick<kF16>(fmt, group, rows, cb); }
