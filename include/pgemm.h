@@ -464,9 +464,18 @@ int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* 
 
 /* Enqueue c[e] = sum over the rows r of expert e of a[r]^T * b[r], zeros for
  * an expert without rows. a: R rows of I; b: R rows of J; c: [E, I, J]. The
- * gradient of w: (a, b) = (x, dy) for PGEMM_B_KN, (dy, x) for PGEMM_B_NK. */
+ * gradient of w: (a, b) = (x, dy) for PGEMM_B_KN, (dy, x) for PGEMM_B_NK.
+ * With few output tiles the rows are cut into pieces whose fp32 sums meet in
+ * `work` (at least the bytes below, free again once the call's work is done)
+ * and are added in order. */
 int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a, int64_t lda, const void* b, int64_t ldb,
-                              const int32_t* offsets, void* c, int64_t R, int64_t E, int64_t I, int64_t J, int dtype);
+                              const int32_t* offsets, void* c, int64_t R, int64_t E, int64_t I, int64_t J, int dtype,
+                              void* work, int64_t work_bytes);
+
+/* Bytes of device scratch that pgemm_grouped_weight_grad needs for these
+ * sizes, at a multiple of 16 (0 where no expert's rows are cut into pieces).
+ * A pure function. */
+int pgemm_grouped_weight_grad_workspace(int64_t R, int64_t E, int64_t I, int64_t J, int64_t* bytes);
 
 /* ---- few rows times 4-bit weights -------------------------------------- */
 

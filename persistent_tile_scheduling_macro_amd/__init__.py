@@ -102,7 +102,9 @@ _moe_combine_backward = _sig("pgemm_moe_combine_backward", _int, _vp, _vp, _i64,
                              _i64, _i64, _int, _vp, _vp)
 _grouped_run = _sig("pgemm_grouped_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int)
 _grouped_weight_grad = _sig("pgemm_grouped_weight_grad", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
-                            _i64, _int)
+                            _i64, _int, _vp, _i64)
+_grouped_weight_grad_workspace = _sig("pgemm_grouped_weight_grad_workspace", _int, _i64, _i64, _i64, _i64,
+                                      ctypes.POINTER(_i64))
 _w4_run = _sig("pgemm_w4_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
@@ -314,10 +316,18 @@ def pgemm_grouped_run(h, x, ldx: int, w, offsets, y, R: int, E: int, K: int, N: 
     _check(_grouped_run(h, _ptr(x), ldx, _ptr(w), _ptr(offsets), _ptr(y), R, E, K, N, layout, dtype), h)
 
 
-def pgemm_grouped_weight_grad(h, a, lda: int, b, ldb: int, offsets, c, R: int, E: int, I: int, J: int,
-                              dtype: int) -> None:
+def pgemm_grouped_weight_grad(h, a, lda: int, b, ldb: int, offsets, c, R: int, E: int, I: int, J: int, dtype: int,
+                              work=None, work_bytes: int = 0) -> None:
     """Enqueue c[e] = a_e^T @ b_e over the rows of each expert."""
-    _check(_grouped_weight_grad(h, _ptr(a), lda, _ptr(b), ldb, _ptr(offsets), _ptr(c), R, E, I, J, dtype), h)
+    _check(_grouped_weight_grad(h, _ptr(a), lda, _ptr(b), ldb, _ptr(offsets), _ptr(c), R, E, I, J, dtype, _ptr(work),
+                                work_bytes), h)
+
+
+def pgemm_grouped_weight_grad_workspace(R: int, E: int, I: int, J: int) -> int:
+    """Bytes of device scratch that pgemm_grouped_weight_grad needs."""
+    v = _i64()
+    _check(_grouped_weight_grad_workspace(int(R), int(E), int(I), int(J), ctypes.byref(v)))
+    return v.value
 
 
 def pgemm_w4_run(h, x, ldx: int, q, scales, zeros, offsets, y, M: int, N: int, K: int, E: int, group: int, fmt: int,

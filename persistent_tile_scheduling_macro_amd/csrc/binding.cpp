@@ -264,9 +264,14 @@ std::tuple<c10::optional<Tensor>, c10::optional<Tensor>> grouped_backward(const 
   if (need_dw) {
     const Tensor &a = nk ? dy : g.x, &b = nk ? g.x : dy;
     dw = make({g.E, a.size(1), b.size(1)}, a, a.scalar_type());
+    int64_t bytes = 0;
+    const int rc = pgemm_grouped_weight_grad_workspace(g.R, g.E, a.size(1), b.size(1), &bytes);
+    if (rc != PGEMM_OK) raise(rc, "gradient of " + num(g.E) + " matrices");
+    Tensor work;
+    if (bytes) work = make({bytes}, a, at::kByte);
     run(a, [&](pgemm_handle_t h) {
       return pgemm_grouped_weight_grad(h, ptr(a), a.stride(0), ptr(b), b.stride(0), ptr<int32_t>(g.offsets), ptr(*dw), g.R, g.E,
-                                       a.size(1), b.size(1), dtype_of(a, "x"));
+                                       a.size(1), b.size(1), dtype_of(a, "x"), bytes ? ptr(work) : nullptr, bytes);
     });
   }
   return {dx, dw};

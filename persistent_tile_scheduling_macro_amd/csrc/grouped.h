@@ -35,6 +35,8 @@ struct Args {
   int N;    // columns of c
   int K;    // rows form: length of the sum (the gradient form has an expert's number of rows)
   int n_n;  // tiles along N
+  int split;   // gradient form: pieces an expert's rows are cut into
+  float* part; // split > 1: their sums, [E][split][M][N rounded up to 8]
 };
 
 // Rows of expert e, bounds kept inside [0, R] whatever offsets hold; e == E
@@ -97,11 +99,12 @@ __device__ inline bool place_tile(const Args& a, int block, Place* p) {
   return false;
 }
 
-// n (up to 8) elements at any even address, the rest zeros.
-__device__ inline u32x4 load_upto(const uint16_t* p, int n) {
+// The last n < 8 elements of a row of `len`, or any 8, the rest zeros. A row of eight is read as its
+// last eight, moved: loads of single elements would wait for each other.
+__device__ inline u32x4 load_upto(const uint16_t* p, int n, int len) {
   if (n >= 8) return moe::load8<false>(p);
-  if (n > 0) return moe::load_part(p, n);
-  return u32x4{0, 0, 0, 0};
+  if (n <= 0) return u32x4{0, 0, 0, 0};
+  return len >= 8 ? moe::shift_down(moe::load8<false>(p + n - 8), 8 - n) : moe::load_part(p, n);
 }
 
 template <int DT>
@@ -110,10 +113,26 @@ __device__ inline u32x4 pack8(floatx4_t a, floatx4_t b) {
   return moe::pack<DT>(f);
 }
 
+// Piece `piece` of an expert's `rows` rows, whole steps of 64: its first row and its rows.
+__device__ inline void piece_rows(const Args& a, int rows, int piece, int* from, int* count) {
+  const int steps = (rows + 63) / 64;
+  const int lo = (int)((int64_t)steps * piece / a.split) * 64, hi = (int)((int64_t)steps * (piece + 1) / a.split) * 64;
+  *from = min(lo, rows);
+  *count = min(hi, rows) - *from;
+}
+__device__ inline int64_t part_row(const Args& a, int e, int piece, int m) {
+  return (((int64_t)e * a.split + piece) * a.M + m) * ((a.N + 7) & ~7);
+}
+
 // The body for operands of any alignment: 128 x 128 tile, four waves of
 // 64 x 64, steps of 64 k. Chunks of eight elements go through registers (the
 // direct load to LDS wants 16-byte addresses): step s+1 is loaded while step
-// s is multiplied, then written to the other LDS stage.
+// s is multiplied, then written to the other LDS stage. A load never waits
+// for another or branches: its address is kept inside the matrix (a chunk over
+// a row's end is read as the row's last eight elements), and what it then has
+// wrong is put right on the way to LDS, in the steps and tiles at an edge
+// only: positions moved, zeros past the sum's end. (Reading the edge element
+// by element took ten times an inner tile's time, and with it the call's.)
 template <int DT, bool GRAD, bool NK>
 __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   constexpr int BM = 128, BN = 128, BK = 64;
@@ -130,19 +149,22 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   int M, K, m0, n0;
   const uint16_t *A, *B;
   uint16_t* C;
+  float* part = nullptr;
   int gap_at = 0, gap = 0; // rows of no expert: from row gap_at on they lie `gap` rows further
   if constexpr (GRAD) {
-    const int n_m = (a.M + BM - 1) / BM, per_expert = n_m * a.n_n;
-    const int e = blockIdx.x / per_expert;
-    int pm, pn, first;
-    grouped_tile(blockIdx.x - e * per_expert, n_m, a.n_n, 8, &pm, &pn);
-    expert_rows(a, e, &first, &K);
+    const int n_m = (a.M + BM - 1) / BM, per = n_m * a.n_n;
+    const int e = blockIdx.x / (per * a.split), u = blockIdx.x - e * per * a.split, piece = u / per;
+    int pm, pn, first, rows, from;
+    grouped_tile(u - piece * per, n_m, a.n_n, 8, &pm, &pn);
+    expert_rows(a, e, &first, &rows);
+    piece_rows(a, rows, piece, &from, &K);
     M = a.M;
     m0 = pm * BM;
     n0 = pn * BN;
-    A = a.a + first * a.lda;
-    B = a.b + first * a.ldb;
+    A = a.a + (first + from) * a.lda;
+    B = a.b + (first + from) * a.ldb;
     C = a.c + (int64_t)e * a.M * a.N;
+    if (a.split > 1) part = a.part + part_row(a, e, piece, 0);
   } else {
     Place p;
     if (!place_tile<BM>(a, blockIdx.x, &p)) return;
@@ -160,24 +182,57 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
       C += (int64_t)p.first * a.N;
     }
   }
-  const int nk = (K + BK - 1) / BK;
+  const int nk = (K + BK - 1) / BK, N = a.N;
 
+  // A thread's chunks of an operand. Rows along k: 128 rows x 8 chunks; else 64 k-rows x 16 chunks.
   u32x4 ra[4], rb[4];
-  // operand rows along k: 128 rows x 8 chunks; else 64 k-rows x 16 chunks
-  auto load_operand = [&](u32x4 (&r)[4], const uint16_t* p, int64_t ld, int o0, int O, int k0, auto kc)
+  auto load_operand = [&](u32x4 (&r)[4], const uint16_t* p, int64_t ld, int o0, int O, int k0, auto kc, auto first)
                           __attribute__((always_inline)) {
+    if constexpr (decltype(kc)::value) {
+      const int k = min(k0 + 8 * (tid & 7), K - 8);
+      if (K < 8) { // fewer than eight in a row
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (decltype(kc)::value) {
-        const int o = o0 + (tid >> 3) + 32 * j, k = k0 + 8 * (tid & 7);
-        r[j] = load_upto(p + o * ld + k, o < O ? K - k : 0);
+        for (int j = 0; j < 4; ++j) r[j] = load_upto(p + min(o0 + (tid >> 3) + 32 * j, O - 1) * ld, tid & 7 ? 0 : K, K);
       } else {
-        const int k = k0 + (tid >> 4) + 16 * j, o = o0 + 8 * (tid & 15);
-        r[j] = load_upto(p + k * ld + o, k < K ? O - o : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = moe::load8<false>(p + min(o0 + (tid >> 3) + 32 * j, O - 1) * ld + k);
+      }
+    } else {
+      const int o = min(o0 + 8 * (tid & 15), O - 8);
+      if (O < 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = load_upto(p + min(k0 + (tid >> 4) + 16 * j, K - 1) * ld, tid & 15 ? 0 : O, O);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) // a sum of few rows (the first step is all) leaves out what lies past them
+          if (!decltype(first)::value || 16 * j < K) r[j] = moe::load8<false>(p + min(k0 + (tid >> 4) + 16 * j, K - 1) * ld + o);
       }
     }
   };
-  auto write_operand = [&](const u32x4 (&r)[4], uint8_t* s, auto kc) __attribute__((always_inline)) {
+  auto write_operand = [&](u32x4 (&r)[4], uint8_t* s, int o0, int O, int k0, auto kc) __attribute__((always_inline)) {
+    const bool last = k0 + BK > K;
+    if constexpr (decltype(kc)::value) {
+      if (last) {
+        const int left = K - k0 - 8 * (tid & 7);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (left <= 0) r[j] = u32x4{0, 0, 0, 0};
+          else if (left < 8 && K >= 8) r[j] = moe::shift_down(r[j], 8 - left);
+        }
+      }
+    } else {
+      if (o0 + 128 > O && O >= 8) { // what lies past O is used for outputs past O only
+        const int left = O - o0 - 8 * (tid & 15);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (left > 0 && left < 8) r[j] = moe::shift_down(r[j], 8 - left);
+      }
+      if (last) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k0 + (tid >> 4) + 16 * j >= K) r[j] = u32x4{0, 0, 0, 0};
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       int at;
@@ -193,13 +248,13 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   };
   typedef std::integral_constant<bool, A_KC> AKC;
   typedef std::integral_constant<bool, B_KC> BKC;
-  auto load = [&](int step) __attribute__((always_inline)) {
-    load_operand(ra, A, a.lda, m0, M, step * BK, AKC{});
-    load_operand(rb, B, a.ldb, n0, a.N, step * BK, BKC{});
+  auto load = [&](int step, auto first) __attribute__((always_inline)) {
+    load_operand(ra, A, a.lda, m0, M, step * BK, AKC{}, first);
+    load_operand(rb, B, a.ldb, n0, N, step * BK, BKC{}, first);
   };
-  auto write = [&](int stage) __attribute__((always_inline)) {
-    write_operand(ra, sA[stage], AKC{});
-    write_operand(rb, sB[stage], BKC{});
+  auto write = [&](int step) __attribute__((always_inline)) {
+    write_operand(ra, sA[step & 1], m0, M, step * BK, AKC{});
+    write_operand(rb, sB[step & 1], n0, N, step * BK, BKC{});
   };
 
   // Fragment offsets. The n-position s16 of block nb is wave column
@@ -229,12 +284,12 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
     for (int j = 0; j < 4; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
   if (nk > 0) {
-    load(0);
+    load(0, std::true_type{});
     write(0);
     __syncthreads();
     for (int s = 0; s < nk; ++s) {
       const bool more = s + 1 < nk;
-      if (more) load(s + 1);
+      if (more) load(s + 1, std::false_type{});
       const uint8_t *pa = sA[s & 1], *pb = sB[s & 1];
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
@@ -248,25 +303,78 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] = mfma(bf[j], af[i], acc[i][j]);
       }
-      if (more) write((s + 1) & 1);
+      if (more) write(s + 1);
       __syncthreads();
     }
   }
 
-  const int n = n0 + wn * 64 + 8 * g;
+  // Output: fp32 sums of a piece go out from the registers; rounded rows are put together in LDS first,
+  // so that 16 lanes store 256 bytes of a row (four lanes and 64 bytes otherwise, which at odd
+  // addresses costs most of the time of a product of few rows).
   const bool odd = (g & 1) != 0;
+  uint8_t* sC = sA[0];
+  static_assert(sizeof(sA) == BM * BN * 2, "the tile's rounded output fits A's stages");
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int q = s16 >> 2;
-    const int m = m0 + wm * 64 + (A_KC ? 16 * i + s16 : 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + (s16 & 3));
-    if (m >= M) continue;
-    uint16_t* row = C + (int64_t)(m < gap_at ? m : m + gap) * a.N;
+    const int m = wm * 64 + (A_KC ? 16 * i + s16 : 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + (s16 & 3));
 #pragma unroll
     for (int P = 0; P < 2; ++P) {
-      const floatx4_t x = acc[i][2 * P], y = acc[i][2 * P + 1];
-      if (n + 32 * P < a.N) moe::store_row<false>(row, n + 32 * P, a.N, odd ? pack8<DT>(y, x) : pack8<DT>(x, y));
+      const floatx4_t x = odd ? acc[i][2 * P + 1] : acc[i][2 * P], y = odd ? acc[i][2 * P] : acc[i][2 * P + 1];
+      const int chunk = wn * 8 + 4 * P + g;
+      if (GRAD && part) {
+        float* to = part + (int64_t)(m0 + m) * ((N + 7) & ~7) + n0 + 8 * chunk;
+        if (m0 + m < M && n0 + 8 * chunk < N) {
+          *reinterpret_cast<floatx4_t*>(to) = x;
+          *reinterpret_cast<floatx4_t*>(to + 4) = y;
+        }
+      } else {
+        *reinterpret_cast<u32x4*>(sC + m * 256 + 16 * (chunk ^ (m & 15))) = pack8<DT>(x, y);
+      }
     }
   }
+  if (GRAD && part) return;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = (tid >> 4) + 16 * j, m = m0 + r, n = n0 + 8 * (tid & 15);
+    if (m < M && n < N)
+      moe::store_row<false>(C + (int64_t)(m < gap_at ? m : m + gap) * N, n, N,
+                            *reinterpret_cast<const u32x4*>(sC + r * 256 + 16 * ((tid & 15) ^ (r & 15))));
+  }
+}
+
+// c[e] = the sum of its pieces' sums, rounded. Eight columns a thread; G threads share their pieces (every
+// G-th), and the first adds the shares in order.
+template <int DT, int G>
+__global__ void __launch_bounds__(256) join_pieces_kernel(Args a) {
+  __shared__ floatx4_t share[G > 1 ? 2 * 256 : 1];
+  const int tid = threadIdx.x, w = tid % (256 / G), group = tid / (256 / G);
+  const int chunks = (a.N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * (256 / G) + w, at = i / chunks;
+  const bool live = at < (int64_t)a.E * a.M;
+  const int n = (int)(i % chunks) * 8, e = (int)(at / a.M), m = (int)(at % a.M);
+  floatx4_t x = {0.f, 0.f, 0.f, 0.f}, y = x;
+  if (live) {
+#pragma unroll 4
+    for (int s = group; s < a.split; s += G) {
+      const float* p = a.part + part_row(a, e, s, m) + n;
+      x += *reinterpret_cast<const floatx4_t*>(p);
+      y += *reinterpret_cast<const floatx4_t*>(p + 4);
+    }
+  }
+  if constexpr (G > 1) {
+    share[tid] = x;
+    share[256 + tid] = y;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int o = 1; o < G; ++o) {
+      x += share[o * (256 / G) + w];
+      y += share[256 + o * (256 / G) + w];
+    }
+  }
+  if (live) moe::store_row<false>(a.c + at * a.N, n, a.N, pack8<DT>(x, y));
 }
 
 // Bodies: this file's, grouped_pp.h's, and grouped_few.h's (rows form) for
@@ -275,6 +383,8 @@ enum Body : int { kAnyAlignment, kPingPong, kFew16, kFew16Wide, kFew32Wide };
 typedef void (*kernel_fn)(Args);
 kernel_fn pick_f16(int body, bool grad, bool nk);
 kernel_fn pick_bf16(int body, bool grad, bool nk);
+kernel_fn join_f16(bool shared); // eight threads to a sum, or one
+kernel_fn join_bf16(bool shared);
 
 } // namespace grouped
 } // namespace pgemm

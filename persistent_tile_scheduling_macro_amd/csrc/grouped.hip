@@ -77,6 +77,37 @@ int pick_rows_body(const grouped::Args& a, bool direct, bool nk) {
   return best;
 }
 
+// Body and pieces of the gradient form, by the same kind of estimate: rounds of workgroups times what one
+// takes (4 us and 1.28 us for 64 rows of a 128 x 128 tile with two on a CU, 1.18 us of a 256 x 256 tile),
+// and what the pieces' sums cost on their way through memory. A piece has 192 rows at least. (One expert,
+// 32768 rows: 64 x 64 647 us in one piece, 512 x 512 653 us, 2048 x 2048 718 us.)
+struct GradPlan { int body; int64_t pieces; };
+GradPlan plan_grad(int64_t R, int64_t E, int64_t I, int64_t J) {
+  GradPlan best = {grouped::kAnyAlignment, 1};
+  double least = 1e30;
+  const double mean = (double)R / E;
+  for (int body : {grouped::kAnyAlignment, grouped::kPingPong}) {
+    if (body == grouped::kPingPong && (I % 8 || J % 8)) continue;
+    const int64_t bm = body == grouped::kPingPong ? 256 : 128, at_once = body == grouped::kPingPong ? 256 : 512;
+    const int64_t tiles = E * ((I + bm - 1) / bm) * ((J + bm - 1) / bm);
+    if (tiles == 0) return best;
+    int64_t fill = at_once / tiles, most = R / E / 192;
+    if (fill > most) fill = most;
+    if (fill > 64) fill = 64;
+    for (int64_t s : {(int64_t)1, fill}) {
+      if (s < 1) continue;
+      const double rounds = (double)((tiles * s + at_once - 1) / at_once);
+      const double t = rounds * (4 + mean / s / 64 * (body == grouped::kPingPong ? 1.18 : 1.28)) +
+                       (s > 1 ? 3 + 8e-6 / 4.5 * s * E * I * J : 0);
+      if (t < least) {
+        least = t;
+        best = {body, s};
+      }
+    }
+  }
+  return best;
+}
+
 // tile_rows(bm): upper bound of the tile rows of height bm over all experts.
 template <class F>
 int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool grad, bool nk) {
@@ -88,8 +119,15 @@ int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool
   else if (!grad) grid = (grid + 7) / 8 * 8;
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
-  const grouped::kernel_fn kern = dtype == PGEMM_F16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(t.threads), 0, h->stream, a);
+  const bool f16 = dtype == PGEMM_F16;
+  hipLaunchKernelGGL(f16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk), dim3((unsigned)grid),
+                     dim3(t.threads), 0, h->stream, a);
+  if (a.split > 1) {
+    const bool shared = a.split >= 8;
+    const int64_t sums = (int64_t)a.E * a.M * ((a.N + 7) / 8), per = shared ? 32 : 256;
+    hipLaunchKernelGGL(f16 ? grouped::join_f16(shared) : grouped::join_bf16(shared), dim3((unsigned)((sums + per - 1) / per)),
+                       dim3(256), 0, h->stream, a);
+  }
   return launch_status(h, "grouped product");
 }
 
@@ -128,14 +166,30 @@ int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* 
   return launch(h, a, pick_rows_body(a, direct, nk), [&](int bm) { return R / bm + E + 1; }, dtype, false, nk);
 }
 
+int pgemm_grouped_weight_grad_workspace(int64_t R, int64_t E, int64_t I, int64_t J, int64_t* bytes) {
+  if (!bytes || R < 0 || E < 1 || I < 0 || J < 0) return PGEMM_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (R > kMaxSize || I > kMaxSize || J > kMaxSize || E > moe::kMaxExperts) return PGEMM_ERR_UNSUPPORTED;
+  const int64_t s = plan_grad(R, E, I, J).pieces;
+  if (s > 1) *bytes = s * E * I * ((J + 7) / 8 * 8) * (int64_t)sizeof(float);
+  return PGEMM_OK;
+}
+
 int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda, const void* b_rows, int64_t ldb,
-                              const int32_t* offsets, void* c, int64_t R, int64_t E, int64_t I, int64_t J, int dtype) {
+                              const int32_t* offsets, void* c, int64_t R, int64_t E, int64_t I, int64_t J, int dtype,
+                              void* work, int64_t work_bytes) {
   if (!h) return PGEMM_ERR_INVALID_ARG;
   h->last_error[0] = 0;
-  const int rc = check(h, R, E, I, J, lda, ldb, dtype);
+  int rc = check(h, R, E, I, J, lda, ldb, dtype);
   if (rc != PGEMM_OK) return rc;
   if (I == 0 || J == 0) return PGEMM_OK;
   if (!offsets || !c || (R > 0 && (!a_rows || !b_rows))) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  int64_t need = 0;
+  rc = pgemm_grouped_weight_grad_workspace(R, E, I, J, &need);
+  if (rc != PGEMM_OK) return rc;
+  if (work_bytes < need || (need && !aligned16(work)) || (need && !work))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "workspace of %lld bytes at %p, %lld at a multiple of 16 are needed",
+                (long long)work_bytes, work, (long long)need);
   grouped::Args a = {};
   a.a = static_cast<const uint16_t*>(a_rows);
   a.b = static_cast<const uint16_t*>(b_rows);
@@ -147,10 +201,13 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda,
   a.E = (int)E;
   a.M = (int)I;
   a.N = (int)J;
+  const GradPlan plan = plan_grad(R, E, I, J);
+  a.split = (int)plan.pieces;
+  a.part = static_cast<float*>(work);
   const bool direct = I % 8 == 0 && J % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && lda <= kMaxDirectStride &&
                       ldb <= kMaxDirectStride && aligned16(a_rows) && aligned16(b_rows) && aligned16(c);
-  const int body = direct && R / E >= 192 ? grouped::kPingPong : grouped::kAnyAlignment;
-  return launch(h, a, body, [&](int bm) { return E * ((I + bm - 1) / bm); }, dtype, true, false);
+  const int body = direct ? plan.body : grouped::kAnyAlignment;
+  return launch(h, a, body, [&](int bm) { return E * a.split * ((I + bm - 1) / bm); }, dtype, true, false);
 }
 
 } // extern "C"

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) grouped_few_kernel(Args a) 
     Slot t;
     if constexpr (NK) {
 #pragma unroll
-      for (int i = 0; i < BLK * L; ++i) t.w[i] = load_upto(w[i] + k0, K - k0 - 8 * chunk);
+      for (int i = 0; i < BLK * L; ++i) t.w[i] = load_upto(w[i] + k0, K - k0 - 8 * chunk, K);
     } else {
       const int left = K - k0 - 8 * g;
 #pragma unroll
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) grouped_few_kernel(Args a) 
       }
     }
 #pragma unroll
-    for (int i = 0; i < MB * L; ++i) t.x[i] = load_upto(x[i] + k0, K - k0 - 8 * chunk);
+    for (int i = 0; i < MB * L; ++i) t.x[i] = load_upto(x[i] + k0, K - k0 - 8 * chunk, K);
     multiply(t);
   }
 

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
   int T; // tiles in all
   const int g_nm = (a.M + BM - 1) / BM; // gradient form: tile rows of every expert
   if constexpr (GRAD) {
-    T = a.E * g_nm * a.n_n;
+    T = a.E * a.split * g_nm * a.n_n;
   } else {
     if (wave == 0) {
       int before = 0;
@@ -80,22 +80,24 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
   struct Tile {
     const uint16_t *A, *B; // row 0 of the tile's rows and columns, k = 0
     int m0, n0, M, K;      // tile origin; rows of c; length of the sum
-    int e, first, gap_at, gap;
+    int e, piece, first, gap_at, gap;
     int nk;                // steps, an even number
   };
   auto tile_at = [&](int t) __attribute__((always_inline)) -> Tile {
     const int u = xcd_remap(t, T, G);
     Tile r;
     int pm, pn;
-    r.gap_at = r.gap = 0;
+    r.gap_at = r.gap = r.piece = 0;
     if constexpr (GRAD) {
-      const int per = g_nm * a.n_n;
-      r.e = u / per;
-      grouped_tile(u - r.e * per, g_nm, a.n_n, 4, &pm, &pn);
-      int first, rows;
+      const int per = g_nm * a.n_n, ep = u / per;
+      r.e = ep / a.split;
+      r.piece = ep - r.e * a.split;
+      grouped_tile(u - ep * per, g_nm, a.n_n, 4, &pm, &pn);
+      int first, rows, from, count;
       expert_rows(a, r.e, &first, &rows);
-      r.first = __builtin_amdgcn_readfirstlane(first);
-      r.K = __builtin_amdgcn_readfirstlane(rows);
+      piece_rows(a, rows, r.piece, &from, &count);
+      r.first = __builtin_amdgcn_readfirstlane(first + from);
+      r.K = __builtin_amdgcn_readfirstlane(count);
       r.M = a.M;
       r.m0 = pm * BM;
       r.n0 = pn * BN;
@@ -137,9 +139,15 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
   // rows of 128 B a block, chunk c of row r at c ^ (r & 7). oc: k-rows, chunk c of
   // row k at c ^ b_swz(k); of the bits that b_swz uses, block j's 8j can set only
   // the one of 8, so B's swizzle changes with j's parity, A's (16j) not at all.
-  const int a_row = A_RPI * wl + lane / (A_ROW / 16), b_row = B_RPI * wl + lane / (B_ROW / 16);
-  const int a_chunk = (lane % (A_ROW / 16)) ^ (A_KC ? a_row & 7 : b_swz<2, A_ROW>(a_row));
-  const int b_chunk = (lane % (B_ROW / 16)) ^ (B_KC ? b_row & 7 : b_swz<2, B_ROW>(b_row));
+  struct Lanes { int a_row, a_chunk, b_row, b_chunk; };
+  auto lanes_of = [&](int l) __attribute__((always_inline)) {
+    Lanes c;
+    c.a_row = A_RPI * wl + l / (A_ROW / 16);
+    c.b_row = B_RPI * wl + l / (B_ROW / 16);
+    c.a_chunk = (l % (A_ROW / 16)) ^ (A_KC ? c.a_row & 7 : b_swz<2, A_ROW>(c.a_row));
+    c.b_chunk = (l % (B_ROW / 16)) ^ (B_KC ? c.b_row & 7 : b_swz<2, B_ROW>(c.b_row));
+    return c;
+  };
 
   // ---- fragment lanes --------------------------------------------------------------
   const int g = lane >> 4, s16 = lane & 15;
@@ -186,9 +194,13 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
     int lda_s = (int)a.lda * 2, ldb_s = (int)a.ldb * 2, wl_s = wl * 1024;
     asm volatile("" : "+s"(lda_s), "+s"(ldb_s), "+s"(wl_s));
     const bool full = (mrem >= 128) & (krem >= BK) & (nrem >= BN);
+    int l = lane;
+    if constexpr (GRAD) // read again each step: kept live, these take the loop past its registers
+      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    const auto [a_row, a_chunk, b_row, b_chunk] = lanes_of(l);
     if constexpr (GR == 0) {
       const __amdgpu_buffer_rsrc_t rb = make_rsrc(u.B + (B_KC ? (int64_t)k0 : k0 * a.ldb));
-      static_for<8>([&](auto jc) __attribute__((always_inline)) {
+      static_for<8>([&, b_row = b_row, b_chunk = b_chunk](auto jc) __attribute__((always_inline)) {
         constexpr int ROW = 4 * B_RPI * decltype(jc)::value;
         int c = b_chunk;
         bool ok;
@@ -204,7 +216,7 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
       });
     }
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(u.A + (A_KC ? 128 * GR * a.lda + k0 : k0 * a.lda + 128 * GR));
-    static_for<4>([&](auto jc) __attribute__((always_inline)) {
+    static_for<4>([&, a_row = a_row, a_chunk = a_chunk](auto jc) __attribute__((always_inline)) {
       constexpr int ROW = 4 * A_RPI * decltype(jc)::value;
       bool ok;
       if constexpr (A_KC) ok = (a_row + ROW < mrem) & (8 * a_chunk < krem);
@@ -262,6 +274,22 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
     const int s16 = lane_e & 15, g = lane_e >> 4, q = s16 >> 2;
     const int n = c.n0 + wl * WN + 8 * g;
     const bool odd = (g & 1) != 0;
+    if constexpr (GRAD) {
+      if (a.split > 1) { // N is a multiple of 8
+        float* part = a.part + part_row(a, c.e, c.piece, 0) + n;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const int m = c.m0 + 128 * GR + 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + (s16 & 3);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) { // block j's columns: the first or the second four of eight
+            const int at = 32 * (j >> 1) + 4 * ((j ^ g) & 1);
+            if (m < c.M && n + 32 * (j >> 1) < a.N) *reinterpret_cast<floatx4_t*>(part + (int64_t)m * a.N + at) = acc_read(acc[i][j]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        return;
+      }
+    }
     out_t* C = reinterpret_cast<out_t*>(a.c) + (GRAD ? (int64_t)c.e * a.M : c.first) * a.N + n;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {

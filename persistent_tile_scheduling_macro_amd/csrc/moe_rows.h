@@ -44,6 +44,18 @@ __device__ inline u32x4 load_part(const uint16_t* p, int n) {
   for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
   return v;
 }
+// The elements from `by` (0..7) on, moved down, zeros behind them.
+__device__ inline u32x4 shift_down(u32x4 v, int by) {
+  uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+  if (by & 4) {
+    lo = hi;
+    hi = 0;
+  }
+  const int bits = 16 * (by & 3);
+  if (bits) lo = lo >> bits | hi << (64 - bits);
+  hi >>= bits;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
 __device__ inline void store_part(uint16_t* p, u32x4 v, int n) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)

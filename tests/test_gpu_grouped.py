@@ -63,6 +63,15 @@ def test_products_and_gradients(moe, counts, K, N, layout, dtype):
 
 
 @pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("counts,K,N", [([1500], 40, 24), ([4100], 64, 64), ([3000, 10, 0], 33, 47), ([5000, 3], 136, 7),
+                                        ([1, 2600], 200, 72), ([0, 900, 2000], 5, 264), ([2049], 131, 135)])
+def test_weight_gradients_over_many_rows(moe, counts, K, N, layout):
+    """Few output tiles: the rows are cut into pieces, of every length with uneven experts."""
+    for dtype in DT.values():
+        check_all(moe, *operands(counts, K, N, layout, dtype, after=2), layout, f"{counts} {K}x{N} {layout} {dtype}")
+
+
+@pytest.mark.parametrize("layout", ["kn", "nk"])
 @pytest.mark.parametrize("counts,K,N", [([5, 3], 64, 72), ([200, 150], 136, 264), ([600, 700], 264, 512), ([40, 9], 33, 17)])
 def test_rows_of_no_expert_give_zeros(moe, counts, K, N, layout):
     x, w, dy, off = operands(counts, K, N, layout, torch.bfloat16, before=3, after=131)
@@ -168,7 +177,8 @@ def test_autograd(moe):
     assert torch.equal(xl.grad, want)
 
 
-@pytest.mark.parametrize("counts,K,N", [([4, 5, 6], 256, 128), ([200, 190, 30], 264, 136), ([800, 300], 512, 520), ([33, 2], 77, 31)])
+@pytest.mark.parametrize("counts,K,N", [([4, 5, 6], 256, 128), ([200, 190, 30], 264, 136), ([800, 300], 512, 520), ([33, 2], 77, 31),
+                                        ([2000, 700], 72, 40)])
 def test_graph_replays_with_other_bounds(moe, counts, K, N):
     """Captured once, replayed with other offsets and rows, eager work between: each replay equals the eager call."""
     x, w, dy, off = operands(counts, K, N, "nk", torch.bfloat16)

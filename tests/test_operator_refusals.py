@@ -67,7 +67,7 @@ def test_python_refuses(error, call):
     lambda: pg.pgemm_moe_combine(None, 0, 8, 0, 0, 1, 1, 8, 0, 0),
     lambda: pg.pgemm_moe_combine_backward(None, 0, 8, 0, 8, 0, 0, 0, 1, 1, 1, 8, 0, 0, 0),
     lambda: pg.pgemm_grouped_run(None, 0, 8, 0, 0, 0, 1, 1, 8, 8, 0, 0),
-    lambda: pg.pgemm_grouped_weight_grad(None, 0, 8, 0, 8, 0, 0, 1, 1, 8, 8, 0),
+    lambda: pg.pgemm_grouped_weight_grad(None, 0, 8, 0, 8, 0, 0, 1, 1, 8, 8, 0, 0, 0),
     lambda: pg.pgemm_w4_run(None, 0, 64, 0, 0, 0, 0, 0, 1, 8, 64, 1, 32, 0, 0),
 ])
 def test_null_handles_are_refused(call):
@@ -85,4 +85,15 @@ def test_dispatch_workspace():
                          ((2 ** 30, 2, 4), pg.PGEMM_ERR_UNSUPPORTED), ((2 ** 40, 1, 4), pg.PGEMM_ERR_UNSUPPORTED)):
         with pytest.raises(pg.PgemmError) as e:
             pg.pgemm_moe_dispatch_workspace(*args)
+        assert e.value.status == status
+
+
+def test_weight_gradient_workspace():
+    size = pg.pgemm_grouped_weight_grad_workspace
+    assert size(0, 4, 64, 64) == 0 and size(100, 4, 64, 64) == 0 and size(32768, 32, 4096, 2048) == 0
+    assert size(32768, 1, 64, 61) % (64 * 64 * 4) == 0 and size(32768, 1, 64, 61) > 0
+    for args, status in (((-1, 1, 8, 8), pg.PGEMM_ERR_INVALID_ARG), ((1, 0, 8, 8), pg.PGEMM_ERR_INVALID_ARG),
+                         ((1, 1025, 8, 8), pg.PGEMM_ERR_UNSUPPORTED), ((2 ** 31, 1, 8, 8), pg.PGEMM_ERR_UNSUPPORTED)):
+        with pytest.raises(pg.PgemmError) as e:
+            size(*args)
         assert e.value.status == status
