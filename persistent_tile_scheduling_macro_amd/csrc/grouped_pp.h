@@ -80,22 +80,22 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
   struct Tile {
     const uint16_t *A, *B; // row 0 of the tile's rows and columns, k = 0
     int m0, n0, M, K;      // tile origin; rows of c; length of the sum
-    int e, piece, first, gap_at, gap;
+    int e, first, gap_at, gap; // e: expert; gradient form: expert * split + piece
     int nk;                // steps, an even number
   };
   auto tile_at = [&](int t) __attribute__((always_inline)) -> Tile {
     const int u = xcd_remap(t, T, G);
     Tile r;
     int pm, pn;
-    r.gap_at = r.gap = r.piece = 0;
+    r.gap_at = r.gap = 0;
     if constexpr (GRAD) {
       const int per = g_nm * a.n_n, ep = u / per;
-      r.e = ep / a.split;
-      r.piece = ep - r.e * a.split;
+      const int e = ep / a.split;
+      r.e = ep;
       grouped_tile(u - ep * per, g_nm, a.n_n, 4, &pm, &pn);
       int first, rows, from, count;
-      expert_rows(a, r.e, &first, &rows);
-      piece_rows(a, rows, r.piece, &from, &count);
+      expert_rows(a, e, &first, &rows);
+      piece_rows(a, rows, ep - e * a.split, &from, &count);
       r.first = __builtin_amdgcn_readfirstlane(first + from);
       r.K = __builtin_amdgcn_readfirstlane(count);
       r.M = a.M;
@@ -139,15 +139,9 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
   // rows of 128 B a block, chunk c of row r at c ^ (r & 7). oc: k-rows, chunk c of
   // row k at c ^ b_swz(k); of the bits that b_swz uses, block j's 8j can set only
   // the one of 8, so B's swizzle changes with j's parity, A's (16j) not at all.
-  struct Lanes { int a_row, a_chunk, b_row, b_chunk; };
-  auto lanes_of = [&](int l) __attribute__((always_inline)) {
-    Lanes c;
-    c.a_row = A_RPI * wl + l / (A_ROW / 16);
-    c.b_row = B_RPI * wl + l / (B_ROW / 16);
-    c.a_chunk = (l % (A_ROW / 16)) ^ (A_KC ? c.a_row & 7 : b_swz<2, A_ROW>(c.a_row));
-    c.b_chunk = (l % (B_ROW / 16)) ^ (B_KC ? c.b_row & 7 : b_swz<2, B_ROW>(c.b_row));
-    return c;
-  };
+  const int b_row = B_RPI * wl + lane / (B_ROW / 16);
+  const int a_row_kept = A_RPI * wl + lane / (A_ROW / 16);
+  const int b_chunk = (lane % (B_ROW / 16)) ^ (B_KC ? b_row & 7 : b_swz<2, B_ROW>(b_row));
 
   // ---- fragment lanes --------------------------------------------------------------
   const int g = lane >> 4, s16 = lane & 15;
@@ -194,13 +188,9 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
     int lda_s = (int)a.lda * 2, ldb_s = (int)a.ldb * 2, wl_s = wl * 1024;
     asm volatile("" : "+s"(lda_s), "+s"(ldb_s), "+s"(wl_s));
     const bool full = (mrem >= 128) & (krem >= BK) & (nrem >= BN);
-    int l = lane;
-    if constexpr (GRAD) // read again each step: kept live, these take the loop past its registers
-      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-    const auto [a_row, a_chunk, b_row, b_chunk] = lanes_of(l);
     if constexpr (GR == 0) {
       const __amdgpu_buffer_rsrc_t rb = make_rsrc(u.B + (B_KC ? (int64_t)k0 : k0 * a.ldb));
-      static_for<8>([&, b_row = b_row, b_chunk = b_chunk](auto jc) __attribute__((always_inline)) {
+      static_for<8>([&](auto jc) __attribute__((always_inline)) {
         constexpr int ROW = 4 * B_RPI * decltype(jc)::value;
         int c = b_chunk;
         bool ok;
@@ -215,8 +205,14 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
                                                  full || ok ? base : kOOB, ROW * ldb_s, 0, 0);
       });
     }
+    int a_row = a_row_kept, l = lane;
+    if constexpr (GRAD) { // read again each step: kept live, these two take the loop past its registers
+      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+      a_row = A_RPI * wl + l / (A_ROW / 16);
+    }
+    const int a_chunk = (l % (A_ROW / 16)) ^ (A_KC ? a_row & 7 : b_swz<2, A_ROW>(a_row));
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(u.A + (A_KC ? 128 * GR * a.lda + k0 : k0 * a.lda + 128 * GR));
-    static_for<4>([&, a_row = a_row, a_chunk = a_chunk](auto jc) __attribute__((always_inline)) {
+    static_for<4>([&](auto jc) __attribute__((always_inline)) {
       constexpr int ROW = 4 * A_RPI * decltype(jc)::value;
       bool ok;
       if constexpr (A_KC) ok = (a_row + ROW < mrem) & (8 * a_chunk < krem);
@@ -276,7 +272,7 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
     const bool odd = (g & 1) != 0;
     if constexpr (GRAD) {
       if (a.split > 1) { // N is a multiple of 8
-        float* part = a.part + part_row(a, c.e, c.piece, 0) + n;
+        float* part = a.part + (int64_t)c.e * a.M * a.N + n;
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
           const int m = c.m0 + 128 * GR + 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + (s16 & 3);
