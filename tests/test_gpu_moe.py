@@ -49,7 +49,8 @@ def sorted_rows(x, order, k):
 
 
 SIZES = [(1, 1, 1, 1), (1, 8, 8, 64), (3, 2, 4, 7), (17, 3, 13, 72), (64, 8, 64, 1021), (256, 8, 8, 64), (257, 8, 16, 33),
-         (300, 11, 40, 136), (2048, 1, 5, 24), (2049, 1, 1024, 24), (700, 9, 1000, 2056), (1500, 4, 3, 1032), (5, 20, 7, 2049)]
+         (300, 11, 40, 136), (2048, 1, 5, 24), (2049, 1, 1024, 24), (700, 9, 1000, 2056), (1500, 4, 3, 1032), (5, 20, 7, 2049),
+         (4096, 4, 300, 40), (5461, 3, 1024, 16), (4097, 4, 64, 40), (9000, 8, 200, 24)]
 
 
 @pytest.mark.parametrize("T,k,E,H", SIZES)
