@@ -31,7 +31,9 @@ namespace w4 {
 
 enum Fmt : int { kInt4 = 0, kInt4Zero = 1, kE2M1 = 2 };
 constexpr int kStep = 128; // k of one load: 4 lane groups x 16 bytes
-constexpr int kWaves = 8;
+// Waves of a workgroup: with 32 rows a wave's operands take 160 registers, and three workgroups of four waves fit a CU
+// where one of eight would.
+constexpr int waves_of(int rows) { return rows == 32 ? 4 : 8; }
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
@@ -131,14 +133,16 @@ __device__ inline float scale_value(uint16_t b) {
 
 // ROWS: rows of x taken at once, 4, 16 or 32 (4 reads only those; the MFMA always has 16).
 template <int DT, int FMT, int GROUP, int ROWS, int CB>
-__global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Args a) {
+__global__ void __launch_bounds__(waves_of(ROWS) * 64, ROWS == 32 ? 3 : 4) w4_kernel(Args a) {
+  constexpr int kWaves = waves_of(ROWS);
   constexpr int MB = (ROWS + 15) / 16, XL = ROWS / 4; // row blocks; loads of x a step
   constexpr int GPS = kStep / GROUP;                  // scale groups of a step
   constexpr int SPG = GROUP / 32;                     // MFMA k-groups of a scale group
   constexpr int GC = 32, CHUNK = GC / GPS;            // scale groups kept at a time, their steps
-  constexpr int D = 2;                                // steps in flight
+  constexpr int D = ROWS == 32 ? 1 : 2; // steps in registers; with 32 rows a step is loaded again as soon as it is in LDS
+  constexpr int XH = ROWS == 32 ? 2 : 1;              // parts in which x goes through LDS
   constexpr int SROW = 2 * GC + 4, ZROW = GC + 4;     // LDS rows of scales and zero points, off the banks' period
-  constexpr int XB = ROWS * 256, WB = CB * 1024, SB = CB * 16 * SROW, ZB = FMT == kInt4Zero ? CB * 16 * ZROW : 0;
+  constexpr int XROW = 256 / XH, XB = ROWS * XROW, WB = CB * 1024, SB = CB * 16 * SROW, ZB = FMT == kInt4Zero ? CB * 16 * ZROW : 0;
   constexpr int TURN = (XB + WB + SB + ZB + 15) / 16 * 16, JOIN = CB * MB * 1024;
   typedef typename Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;
@@ -167,8 +171,9 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
   if (m0 >= m1) return;
 
   uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + XB, *turn_s = turn_w + WB, *turn_z = turn_s + SB;
-  // a load's lanes: four to a column (codes, scales), 16 to a row of x
-  const int wcol = lane >> 2, wpart = lane & 3, xr = lane >> 4, xpart = lane & 15;
+  // a load's lanes: four to a column (codes, scales), 16 to a row of x (8 where x goes in two parts)
+  constexpr int XC = 16 / XH, XR = 64 / XC; // chunks of a row part, rows of a load
+  const int wcol = lane >> 2, wpart = lane & 3, xr = lane / XC, xpart = lane % XC;
   const uint8_t* wp[CB];
   auto column = [&](int c) __attribute__((always_inline)) { // columns past N read the last one and are not stored
     return (int64_t)e * a.N + min(n0 + 16 * c + wcol, a.N - 1);
@@ -179,6 +184,7 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
   const int whole = a.K / kStep;
   const int first = (int)((int64_t)wave * whole / kWaves), last = (int)((int64_t)(wave + 1) * whole / kWaves);
 
+  auto x_swizzle = [](int row) __attribute__((always_inline)) { return XROW == 256 ? 2 * (row & 7) : row & 7; };
   auto wave_fence = [&]() __attribute__((always_inline)) { // LDS serves a wave in order: only the compiler has to be held
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -190,19 +196,22 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
     for (int b = 0; b < MB; ++b)
 #pragma unroll
       for (int c = 0; c < CB; ++c) acc[b][c] = d[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* xp[XL];
+    const uint16_t* xp[XL / XH];
 #pragma unroll
-    for (int i = 0; i < XL; ++i) // rows past the last read the last one and are not stored
-      xp[i] = a.x + min(m0 + 4 * i + xr, m1 - 1) * a.ldx + 8 * xpart;
+    for (int i = 0; i < XL / XH; ++i) // rows past the last read the last one and are not stored
+      xp[i] = a.x + min(m0 + XR * i + xr, m1 - 1) * a.ldx + 8 * xpart;
 
     struct Step { // what one step reads
-      u32x4 w[CB], x[XL];
+      u32x4 w[CB], x[XH][XL / XH];
     };
     auto load = [&](Step& t, int step) __attribute__((always_inline)) {
 #pragma unroll
       for (int c = 0; c < CB; ++c) t.w[c] = *reinterpret_cast<const u32x4_any*>(wp[c] + (int64_t)step * (kStep / 2));
 #pragma unroll
-      for (int i = 0; i < XL; ++i) t.x[i] = *reinterpret_cast<const u32x4_any*>(xp[i] + (int64_t)step * kStep);
+      for (int h = 0; h < XH; ++h)
+#pragma unroll
+        for (int i = 0; i < XL / XH; ++i)
+          t.x[h][i] = *reinterpret_cast<const u32x4_any*>(xp[i] + (int64_t)step * kStep + h * (kStep / XH));
     };
     // scales and zero points of the GC groups from step's first on
     auto refill = [&](int step) __attribute__((always_inline)) {
@@ -233,12 +242,15 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
       }
     };
     auto compute = [&](Step& t, int step) __attribute__((always_inline)) {
-      wave_fence(); // the last step's reads come first
+      auto write_x = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < XL; ++i) {
-        const int r = 4 * i + xr;
-        *reinterpret_cast<u32x4*>(turn_x + r * 256 + 16 * (xpart ^ (2 * (r & 7)))) = t.x[i];
-      }
+        for (int i = 0; i < XL / XH; ++i) {
+          const int r = XR * i + xr;
+          *reinterpret_cast<u32x4*>(turn_x + r * XROW + 16 * (xpart ^ x_swizzle(r))) = t.x[h][i];
+        }
+      };
+      wave_fence(); // the last step's reads come first
+      write_x(0);
 #pragma unroll
       for (int c = 0; c < CB; ++c)
         *reinterpret_cast<u32x4*>(turn_w + c * 1024 + wcol * 64 + 16 * (wpart ^ (wcol >> 2))) = t.w[c];
@@ -247,12 +259,18 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
       const int gr = (step - first) % CHUNK * GPS;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (XH == 2 && i == 2) {
+          wave_fence();
+          write_x(1);
+          load(t, min(step + D, last - 1)); // past the range the last one again, not used
+          wave_fence();
+        }
         frag_t xo[MB];
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
-          const int r = ROWS == 4 ? s & 3 : 16 * b + s;
+          const int r = ROWS == 4 ? s & 3 : 16 * b + s, chunk = 4 * (i % (4 / XH)) + g;
           xo[b] = __builtin_bit_cast(
-              frag_t, order_x<DT, FMT>(*reinterpret_cast<const u32x4*>(turn_x + r * 256 + 16 * ((4 * i + g) ^ (2 * (r & 7))))));
+              frag_t, order_x<DT, FMT>(*reinterpret_cast<const u32x4*>(turn_x + r * XROW + 16 * (chunk ^ x_swizzle(r)))));
         }
 #pragma unroll
         for (int c = 0; c < CB; ++c) {
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(kWaves * 64, ROWS == 32 ? 2 : 4) w4_kernel(Arg
 #pragma unroll
         for (int j = 0; j < D; ++j) {
           if (i + j < last) compute(t[j], i + j);
-          load(t[j], min(i + j + D, last - 1)); // past the range the last one again, not used
+          if (XH == 1) load(t[j], min(i + j + D, last - 1));
         }
       }
     }

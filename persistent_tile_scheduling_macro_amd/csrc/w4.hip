@@ -56,7 +56,7 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   const int form = zeros ? w4::kInt4Zero : fmt == PGEMM_W4_E2M1 ? w4::kE2M1 : w4::kInt4;
   const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, rows, cb) : w4::pick_bf16(form, group, rows, cb);
   if (row_groups <= 65535) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::kWaves * 64), 0, h->stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::waves_of(rows) * 64), 0, h->stream, a);
     return launch_status(h, "w4");
   }
   // more rows than one grid has: launches of at most 65535 row groups each
@@ -66,7 +66,7 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
     b.x = a.x + from * ldx;
     b.y = a.y + from * N;
     b.M = (int)(M - from < count * rows ? M - from : count * rows);
-    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)count), dim3(w4::kWaves * 64), 0, h->stream, b);
+    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)count), dim3(w4::waves_of(rows) * 64), 0, h->stream, b);
   }
   return launch_status(h, "w4");
 }
