@@ -102,9 +102,9 @@ __device__ inline bool place_tile(const Args& a, int block, Place* p) {
 // The last n < 8 elements of a row of `len`, or any 8, the rest zeros. A row of eight is read as its
 // last eight, moved: loads of single elements would wait for each other.
 __device__ inline u32x4 load_upto(const uint16_t* p, int n, int len) {
-  if (n >= 8) return moe::load8<false>(p);
+  if (n >= 8) return moe::load8<moe::kAnyAddress>(p);
   if (n <= 0) return u32x4{0, 0, 0, 0};
-  return len >= 8 ? moe::shift_down(moe::load8<false>(p + n - 8), 8 - n) : moe::load_part(p, n);
+  return len >= 8 ? moe::shift_down(moe::load8<moe::kAnyAddress>(p + n - 8), 8 - n) : moe::load_part(p, n);
 }
 
 template <int DT>
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
         for (int j = 0; j < 4; ++j) r[j] = load_upto(p + min(o0 + (tid >> 3) + 32 * j, O - 1) * ld, tid & 7 ? 0 : K, K);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = moe::load8<false>(p + min(o0 + (tid >> 3) + 32 * j, O - 1) * ld + k);
+        for (int j = 0; j < 4; ++j) r[j] = moe::load8<moe::kAnyAddress>(p + min(o0 + (tid >> 3) + 32 * j, O - 1) * ld + k);
       }
     } else {
       const int o = min(o0 + 8 * (tid & 15), O - 8);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) // a sum of few rows (the first step is all) leaves out what lies past them
-          if (!decltype(first)::value || 16 * j < K) r[j] = moe::load8<false>(p + min(k0 + (tid >> 4) + 16 * j, K - 1) * ld + o);
+          if (!decltype(first)::value || 16 * j < K) r[j] = moe::load8<moe::kAnyAddress>(p + min(k0 + (tid >> 4) + 16 * j, K - 1) * ld + o);
       }
     }
   };
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(256, 2) grouped_kernel(Args a) {
   for (int j = 0; j < 8; ++j) {
     const int r = (tid >> 4) + 16 * j, m = m0 + r, n = n0 + 8 * (tid & 15);
     if (m < M && n < N)
-      moe::store_row<false>(C + (int64_t)(m < gap_at ? m : m + gap) * N, n, N,
+      moe::store_row<moe::kAnyAddress>(C + (int64_t)(m < gap_at ? m : m + gap) * N, n, N,
                             *reinterpret_cast<const u32x4*>(sC + r * 256 + 16 * ((tid & 15) ^ (r & 15))));
   }
 }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(Args a) {
       y += share[256 + o * (256 / G) + w];
     }
   }
-  if (live) moe::store_row<false>(a.c + at * a.N, n, a.N, pack8<DT>(x, y));
+  if (live) moe::store_row<moe::kAnyAddress>(a.c + at * a.N, n, a.N, pack8<DT>(x, y));
 }
 
 // Bodies: this file's, grouped_pp.h's, and grouped_few.h's (rows form) for

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) grouped_few_kernel(Args a) 
     const int64_t k0 = (int64_t)step * STEP;
     if constexpr (NK) {
 #pragma unroll
-      for (int i = 0; i < BLK * L; ++i) t.w[i] = moe::load8<false>(w[i] + k0);
+      for (int i = 0; i < BLK * L; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
     } else {
       const uint16_t* r = w[0] + k0 * a.ldb;
 #pragma unroll
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) grouped_few_kernel(Args a) 
       }
     }
 #pragma unroll
-    for (int i = 0; i < MB * L; ++i) t.x[i] = moe::load8<false>(x[i] + k0);
+    for (int i = 0; i < MB * L; ++i) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
   };
   floatx4_t acc[MB][BLK];
 #pragma unroll

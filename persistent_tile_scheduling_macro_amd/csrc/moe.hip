@@ -28,6 +28,12 @@ int check_experts(pgemm_ctx* h, int64_t E) {
   return PGEMM_OK;
 }
 
+// How the kernels touch the n sorted rows.
+int access_of(bool aligned, int64_t n, int64_t H) {
+  constexpr int64_t cache = (int64_t)256 << 20; // the memory-side cache
+  return !aligned ? moe::kAnyAddress : n * H * 2 > cache && H > 1024 ? moe::kStream : moe::kAligned;
+}
+
 bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
 
 // Slots a workgroup of the sort takes: kTile, or more where that would make too many workgroups.
@@ -44,10 +50,10 @@ unsigned token_blocks(int64_t T, int64_t H) {
 }
 
 template <class ID>
-void launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, bool al) {
+void launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, int access) {
   const hipStream_t st = h->stream;
   if (s.n <= kSmallSlots) {
-    auto kern = al ? moe::dispatch_small_kernel<ID, true> : moe::dispatch_small_kernel<ID, false>;
+    auto kern = access ? moe::dispatch_small_kernel<ID, moe::kAligned> : moe::dispatch_small_kernel<ID, moe::kAnyAddress>;
     hipLaunchKernelGGL(kern, dim3((unsigned)a.T + 1), dim3(moe::kThreads), 0, st, s, a);
     return;
   }
@@ -58,12 +64,13 @@ void launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, bool
   a.token_blocks = (int)token_blocks(a.T, a.H);
   const dim3 grid((unsigned)a.token_blocks + kClearBlocks);
   const bool wide = lanes_of(a.H) == 256;
-  auto kern = al ? (wide ? moe::move_kernel<true, 256> : moe::move_kernel<true, 64>)
-                 : (wide ? moe::move_kernel<false, 256> : moe::move_kernel<false, 64>);
+  auto kern = access == moe::kStream    ? moe::move_kernel<moe::kStream, 256>
+              : access == moe::kAligned ? (wide ? moe::move_kernel<moe::kAligned, 256> : moe::move_kernel<moe::kAligned, 64>)
+                                        : (wide ? moe::move_kernel<moe::kAnyAddress, 256> : moe::move_kernel<moe::kAnyAddress, 64>);
   hipLaunchKernelGGL(kern, grid, dim3(moe::kThreads), 0, st, a);
 }
 
-template <int DT, bool AL, int LANES, bool WEIGHTED>
+template <int DT, int AL, int LANES, bool WEIGHTED>
 void launch_sum_k(pgemm_ctx* h, const moe::SumArgs& a, unsigned grid) {
   auto kern = a.k >= 8   ? moe::gather_sum_kernel<DT, AL, LANES, 8, WEIGHTED>
               : a.k >= 3 ? moe::gather_sum_kernel<DT, AL, LANES, 4, WEIGHTED>
@@ -71,23 +78,18 @@ void launch_sum_k(pgemm_ctx* h, const moe::SumArgs& a, unsigned grid) {
   hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
 }
 
-template <bool WEIGHTED>
-void launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int dtype, bool al) {
+template <int DT, bool WEIGHTED>
+void launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int access) {
   const unsigned grid = token_blocks(a.T, a.H);
-  const int form = (dtype == PGEMM_BF16 ? 4 : 0) + (al ? 2 : 0) + (lanes_of(a.H) == 256 ? 1 : 0);
-  switch (form) {
-    case 0: return launch_sum_k<kF16, false, 64, WEIGHTED>(h, a, grid);
-    case 1: return launch_sum_k<kF16, false, 256, WEIGHTED>(h, a, grid);
-    case 2: return launch_sum_k<kF16, true, 64, WEIGHTED>(h, a, grid);
-    case 3: return launch_sum_k<kF16, true, 256, WEIGHTED>(h, a, grid);
-    case 4: return launch_sum_k<kBF16, false, 64, WEIGHTED>(h, a, grid);
-    case 5: return launch_sum_k<kBF16, false, 256, WEIGHTED>(h, a, grid);
-    case 6: return launch_sum_k<kBF16, true, 64, WEIGHTED>(h, a, grid);
-    default: return launch_sum_k<kBF16, true, 256, WEIGHTED>(h, a, grid);
-  }
+  const bool wide = lanes_of(a.H) == 256;
+  if (access == moe::kStream) return launch_sum_k<DT, moe::kStream, 256, WEIGHTED>(h, a, grid);
+  if (access == moe::kAligned)
+    return wide ? launch_sum_k<DT, moe::kAligned, 256, WEIGHTED>(h, a, grid) : launch_sum_k<DT, moe::kAligned, 64, WEIGHTED>(h, a, grid);
+  return wide ? launch_sum_k<DT, moe::kAnyAddress, 256, WEIGHTED>(h, a, grid)
+              : launch_sum_k<DT, moe::kAnyAddress, 64, WEIGHTED>(h, a, grid);
 }
 
-template <int DT, bool AL, int LANES>
+template <int DT, int AL, int LANES>
 void launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
   auto kern = a.k >= 8   ? moe::combine_backward_kernel<DT, AL, LANES, 8>
               : a.k >= 3 ? moe::combine_backward_kernel<DT, AL, LANES, 4>
@@ -95,19 +97,14 @@ void launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
   hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
 }
 
-void launch_back(pgemm_ctx* h, const moe::BackArgs& a, int dtype, bool al) {
+template <int DT>
+void launch_back(pgemm_ctx* h, const moe::BackArgs& a, int access) {
   const unsigned grid = (unsigned)a.token_blocks + kClearBlocks;
-  const int form = (dtype == PGEMM_BF16 ? 4 : 0) + (al ? 2 : 0) + (lanes_of(a.H) == 256 ? 1 : 0);
-  switch (form) {
-    case 0: return launch_back_k<kF16, false, 64>(h, a, grid);
-    case 1: return launch_back_k<kF16, false, 256>(h, a, grid);
-    case 2: return launch_back_k<kF16, true, 64>(h, a, grid);
-    case 3: return launch_back_k<kF16, true, 256>(h, a, grid);
-    case 4: return launch_back_k<kBF16, false, 64>(h, a, grid);
-    case 5: return launch_back_k<kBF16, false, 256>(h, a, grid);
-    case 6: return launch_back_k<kBF16, true, 64>(h, a, grid);
-    default: return launch_back_k<kBF16, true, 256>(h, a, grid);
-  }
+  const bool wide = lanes_of(a.H) == 256;
+  if (access == moe::kStream) return launch_back_k<DT, moe::kStream, 256>(h, a, grid);
+  if (access == moe::kAligned)
+    return wide ? launch_back_k<DT, moe::kAligned, 256>(h, a, grid) : launch_back_k<DT, moe::kAligned, 64>(h, a, grid);
+  return wide ? launch_back_k<DT, moe::kAnyAddress, 256>(h, a, grid) : launch_back_k<DT, moe::kAnyAddress, 64>(h, a, grid);
 }
 
 int sum_impl(pgemm_handle_t h, const void* rows, int64_t ld, const float* w, const int32_t* pos, int64_t T, int64_t k,
@@ -132,8 +129,9 @@ int sum_impl(pgemm_handle_t h, const void* rows, int64_t ld, const float* w, con
   a.H = (int)H;
   a.n = (int)(T * k);
   const bool al = H % 8 == 0 && ld % 8 == 0 && aligned16(rows) && aligned16(out);
-  if (weighted) launch_sum<true>(h, a, dtype, al);
-  else launch_sum<false>(h, a, dtype, al);
+  const int access = access_of(al, T * k, H);
+  if (dtype == PGEMM_BF16) weighted ? launch_sum<kBF16, true>(h, a, access) : launch_sum<kBF16, false>(h, a, access);
+  else weighted ? launch_sum<kF16, true>(h, a, access) : launch_sum<kF16, false>(h, a, access);
   return launch_status(h, weighted ? "combine" : "dispatch backward");
 }
 
@@ -196,8 +194,9 @@ int pgemm_moe_dispatch(pgemm_handle_t h, const void* x, int64_t ldx, const void*
   a.n = s.n;
   a.token_blocks = 0;
   const bool al = H % 8 == 0 && ldx % 8 == 0 && aligned16(x) && aligned16(xs);
-  if (ids_type == PGEMM_IDS_I32) launch_dispatch<int32_t>(h, s, a, al);
-  else launch_dispatch<int64_t>(h, s, a, al);
+  const int access = access_of(al, T * k, H);
+  if (ids_type == PGEMM_IDS_I32) launch_dispatch<int32_t>(h, s, a, access);
+  else launch_dispatch<int64_t>(h, s, a, access);
   return launch_status(h, "dispatch");
 }
 
@@ -243,7 +242,9 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
   a.n = (int)(T * k);
   a.token_blocks = (int)token_blocks(T, H);
   const bool al = H % 8 == 0 && lddout % 8 == 0 && ldys % 8 == 0 && aligned16(dout) && aligned16(ys) && aligned16(dys);
-  launch_back(h, a, dtype, al);
+  const int access = access_of(al, T * k, H);
+  if (dtype == PGEMM_BF16) launch_back<kBF16>(h, a, access);
+  else launch_back<kF16>(h, a, access);
   return launch_status(h, "combine backward");
 }
 

@@ -21,17 +21,27 @@ constexpr int kMaxChunks = 256;    // workgroups of the sort (each reads all of 
 // Eight 16-bit elements. Rows whose length is no multiple of 8 start at any
 // even address; gfx950 serves wide global accesses at such addresses, so
 // both forms move 16 bytes a lane (AL only tells the compiler the alignment).
+// kStream marks accesses that the memory-side cache should not keep: sorted
+// rows of more bytes than it holds (256 MiB) are gone before anyone reads them
+// again, but on their way push out what would be, and their writing back
+// delays the next kernel. 65536 rows of 4096 bf16, dispatch and its gradient:
+// 104 + 162 us with plain accesses, 105 + 109 us streamed; combine and its
+// gradients 143 + 216 and 112 + 222. Rows that fit are faster kept (12297 of
+// 2056 fp16: 13.5 + 21.6 us against 16.5 + 25.6).
+enum Access : int { kAnyAddress = 0, kAligned = 1, kStream = 2 };
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
-template <bool AL>
+template <int AL>
 __device__ inline u32x4 load8(const uint16_t* p) {
-  if constexpr (AL) return *reinterpret_cast<const u32x4*>(p);
+  if constexpr (AL == kStream) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else if constexpr (AL) return *reinterpret_cast<const u32x4*>(p);
   else return *reinterpret_cast<const u32x4_any*>(p);
 }
-template <bool AL>
+template <int AL>
 __device__ inline void store8(uint16_t* p, u32x4 v) {
-  if constexpr (AL) *reinterpret_cast<u32x4*>(p) = v;
+  if constexpr (AL == kStream) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else if constexpr (AL) *reinterpret_cast<u32x4*>(p) = v;
   else *reinterpret_cast<u32x4_any*>(p) = v;
 }
 // The last elements of a row: n < 8 of them, the rest read as zeros.
@@ -61,11 +71,11 @@ __device__ inline void store_part(uint16_t* p, u32x4 v, int n) {
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
 }
-template <bool AL>
+template <int AL>
 __device__ inline u32x4 load_row(const uint16_t* row, int h, int H) {
   return AL || h + 8 <= H ? load8<AL>(row + h) : load_part(row + h, H - h);
 }
-template <bool AL>
+template <int AL>
 __device__ inline void store_row(uint16_t* row, int h, int H, u32x4 v) {
   if (AL || h + 8 <= H) store8<AL>(row + h, v);
   else store_part(row + h, v, H - h);
@@ -266,14 +276,14 @@ __device__ inline void clear_tail(uint16_t* rows, const int* offsets, int E, int
   kept = kept < 0 ? 0 : kept > n ? n : kept;
   const int64_t from = (int64_t)kept * H, to = (int64_t)n * H;
   for (int64_t i = from + ((int64_t)part * kThreads + threadIdx.x) * 8; i < to; i += (int64_t)parts * kThreads * 8) {
-    if (i + 8 <= to) store8<false>(rows + i, u32x4{0, 0, 0, 0});
+    if (i + 8 <= to) store8<kAnyAddress>(rows + i, u32x4{0, 0, 0, 0});
     else store_part(rows + i, u32x4{0, 0, 0, 0}, (int)(to - i));
   }
 }
 
 // LANES lanes carry one token: its row is read once and written to the
 // position of each of its slots.
-template <bool AL, int LANES>
+template <int AL, int LANES>
 __global__ void __launch_bounds__(kThreads) move_kernel(MoveArgs a) {
   if ((int)blockIdx.x >= a.token_blocks) {
     clear_tail(a.xs, a.offsets, a.E, a.n, a.H, blockIdx.x - a.token_blocks, gridDim.x - a.token_blocks);
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(MoveArgs a) {
   const uint16_t* row = a.x + t * a.ldx;
   const int* pos = a.pos + t * a.k;
   for (int h = (threadIdx.x % LANES) * 8; h < a.H; h += LANES * 8) {
-    const u32x4 v = load_row<AL>(row, h, a.H);
+    const u32x4 v = load_row<AL != 0>(row, h, a.H);
     for (int j = 0; j < a.k; ++j) {
       const int p = pos[j];
       if ((unsigned)p < (unsigned)a.n) store_row<AL>(a.xs + (int64_t)p * a.H, h, a.H, v);
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(MoveArgs a) {
 // finds the positions of its own slots by comparing them with every other
 // (n*k/256 compares a thread, no wait for another workgroup), then moves the
 // row. The last workgroup writes the offsets.
-template <class ID, bool AL>
+template <class ID, int AL>
 __global__ void __launch_bounds__(kThreads) dispatch_small_kernel(SortArgs s, MoveArgs a) {
   __shared__ int cnt[kMaxExperts + 1];
   __shared__ int part[4];
@@ -377,7 +387,7 @@ struct SumArgs {
 // rounded once. KU rows are read at a time; a dropped slot reads row 0 (which
 // stays in the caches) and counts as zero whatever its weight or that row
 // hold, so that the loads of a group need no branch between them.
-template <int DT, bool AL, int LANES, int KU, bool WEIGHTED>
+template <int DT, int AL, int LANES, int KU, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
   if (t >= a.T) return;
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a) {
         for (int i = 0; i < 8; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
       }
     }
-    store_row<AL>(out, h, a.H, pack<DT>(acc));
+    store_row<AL != 0>(out, h, a.H, pack<DT>(acc));
   }
 }
 
@@ -427,7 +437,7 @@ struct BackArgs {
 // token's gradient is read once for up to KU slots, each slot's row of ys
 // once. The products of a dot are added in fp32 in a fixed order (lane,
 // wave, workgroup).
-template <int DT, bool AL, int LANES, int KU>
+template <int DT, int AL, int LANES, int KU>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(BackArgs a) {
   __shared__ float part[kThreads / 64][KU];
   if ((int)blockIdx.x >= a.token_blocks) {
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(BackArgs a) 
     if (live) {
       for (int h = (threadIdx.x % LANES) * 8; h < a.H; h += LANES * 8) {
         u32x4 y[KU];
-        const u32x4 g = load_row<AL>(dout, h, a.H);
+        const u32x4 g = load_row<AL != 0>(dout, h, a.H);
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
           y[u] = load_row<AL>(a.ys + (ok[u] ? (int64_t)p[u] * a.ldys : 0), h, a.H);
