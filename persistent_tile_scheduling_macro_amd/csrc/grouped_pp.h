@@ -11,6 +11,16 @@
 //   read by the transposing LDS reads like a K x N B.
 // * A tile without a sum (an expert or a gap without rows to sum over) runs
 //   two steps whose copies are all masked and read zeros.
+//
+// 32768 rows over 32 experts, 4096 x 2048 bf16: forward and rows' gradient 503
+// to 510 us (1080 TFLOP/s, MFMAs busy 0.55 to 0.59 at the clock that power
+// allows; torch's product of 8192^3 runs at 1222 on the same card), weight
+// gradient 640 us (860): its tiles sum 16 steps only and store 128 KiB each,
+// 537 MB in all. Measured and not kept: tile heights that divide an expert's
+// rows evenly with the MFMAs of empty row blocks left out (the jumps between
+// the MFMAs cost 7% of full tiles, and partial tiles, whose copies and reads
+// bound them, gained nothing); nontemporal stores of c (6% slower: a store
+// covers half lines); a tile's stores after the next tile's copies (spills).
 #pragma once
 
 #include "gemm_pingpong.h"

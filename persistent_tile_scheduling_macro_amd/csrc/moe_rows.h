@@ -5,7 +5,10 @@
 //   p(s) = #{s' : key(s') < key(s)} + #{s' < s : key(s') = key(s)},
 // a stable counting sort, so no result depends on the order in which
 // workgroups run. Everything here moves rows or sums at most a few of them:
-// the bytes of the sorted rows bound every kernel.
+// the bytes of the sorted rows bound every kernel. 8192 tokens x 8 of 64
+// experts, rows of 4096 bf16: the sort 6 + 10 us, the rows moved 103 us (5.9
+// TB/s of reads and writes), gathered and summed 109 to 112 us (5.4 to 5.6),
+// both gradients of combine 221 us (5.2); a large copy reaches 5.2.
 #pragma once
 
 #include "device_common.h"

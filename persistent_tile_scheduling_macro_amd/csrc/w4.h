@@ -14,6 +14,8 @@
 //           in one scale group;
 //   x       16 lanes read 256 bytes of a row; operands of 16 bytes;
 //   scales, zero points   read for 32 groups at a time.
+// 16 x 16384 x 8192 with zero points now takes 22 us (3.6 TB/s), e2m1 without 18.8
+// us; decoding and the turns through LDS keep it from the reads' own 13 us.
 //
 // Codes become operands without rounding: code - z is a whole number up to
 // 15 and an e2m1 value has two significant bits, so both are exact in either
