@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(Args a) {
 }
 
 // Bodies: this file's, grouped_pp.h's, and grouped_few.h's (rows form) for
-// 16 or 32 rows at once, with one or two column blocks of N x K weights.
-enum Body : int { kAnyAlignment, kPingPong, kFew16, kFew16Wide, kFew32Wide };
+// 16 or 32 rows at once, with one or two column blocks of N x K weights, and for
+// the weight gradient of few rows.
+enum Body : int { kAnyAlignment, kPingPong, kFew16, kFew16Wide, kFew32Wide, kFewGrad };
 typedef void (*kernel_fn)(Args);
 kernel_fn pick_f16(int body, bool grad, bool nk);
 kernel_fn pick_bf16(int body, bool grad, bool nk);

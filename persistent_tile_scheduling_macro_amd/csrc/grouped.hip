@@ -30,6 +30,7 @@ Shape shape_of(int body, bool nk) {
     case grouped::kFew16: return {16, nk ? 16 : 64, 512};
     case grouped::kFew16Wide: return {16, nk ? 32 : 64, 512};
     case grouped::kFew32Wide: return {32, nk ? 32 : 64, 512};
+    case grouped::kFewGrad: return {128, 128, 512};
     default: return {128, 128, 256};
   }
 }
@@ -83,6 +84,7 @@ int pick_rows_body(const grouped::Args& a, bool direct, bool nk) {
 // 32768 rows: 64 x 64 647 us in one piece, 512 x 512 653 us, 2048 x 2048 718 us.)
 struct GradPlan { int body; int64_t pieces; };
 GradPlan plan_grad(int64_t R, int64_t E, int64_t I, int64_t J) {
+  if (R / E <= 32) return {grouped::kFewGrad, 1};
   GradPlan best = {grouped::kAnyAlignment, 1};
   double least = 1e30;
   const double mean = (double)R / E;
@@ -206,7 +208,7 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda,
   a.part = static_cast<float*>(work);
   const bool direct = I % 8 == 0 && J % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && lda <= kMaxDirectStride &&
                       ldb <= kMaxDirectStride && aligned16(a_rows) && aligned16(b_rows) && aligned16(c);
-  const int body = direct ? plan.body : grouped::kAnyAlignment;
+  const int body = direct || plan.body == grouped::kFewGrad ? plan.body : grouped::kAnyAlignment;
   return launch(h, a, body, [&](int bm) { return E * a.split * ((I + bm - 1) / bm); }, dtype, true, false);
 }
 

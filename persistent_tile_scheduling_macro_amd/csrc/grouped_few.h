@@ -208,5 +208,77 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) grouped_few_kernel(Args a) 
   }
 }
 
+// The gradient form for experts of few rows: writing c bounds it, and what
+// keeps the writes going is many tiles in flight. So steps are 32 rows (one
+// MFMA's depth), LDS holds one step or the rounded tile (32 KiB) and a wave
+// 64 x 32 of the 128 x 128 tile: three workgroups of eight waves to a CU, where
+// the any-alignment body has two of four. 27 experts of some five rows,
+// 3224 x 2968 bf16 (516 MB of c): 147 us there, LATER us here.
+template <int DT>
+__global__ void __launch_bounds__(512, 6) grad_few_kernel(Args a) {
+  constexpr int BM = 128, BN = 128, BK = 32, ROW = 256;
+  typedef typename fast::Frag<DT>::t frag_t;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[BM * BN * 2];
+  uint8_t *sA = lds, *sB = lds + BK * ROW;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
+  const int g = lane >> 4, q = (lane & 15) >> 2, qt = lane & 3;
+  const int M = a.M, N = a.N, n_m = (M + BM - 1) / BM, per = n_m * a.n_n;
+  const int e = blockIdx.x / per;
+  int pm, pn, first, K;
+  grouped_tile(blockIdx.x - e * per, n_m, a.n_n, 8, &pm, &pn);
+  expert_rows(a, e, &first, &K);
+  const int m0 = pm * BM, n0 = pn * BN;
+
+  // a thread's chunk of a step: row tid / 16, eight elements of each operand
+  const int kr = tid >> 4, m_at = m0 + 8 * (tid & 15), n_at = n0 + 8 * (tid & 15);
+  const int at = kr * ROW + 16 * ((tid & 15) ^ b_swz<2, ROW>(kr));
+  const int k = 8 * g + q; // fragment row; oc order of grouped.h
+  const int frag_at = k * ROW + 16 * (qt ^ b_swz<2, ROW>(k)) + 8 * (qt & 1);
+  auto block = [](int i) __attribute__((always_inline)) { return 64 * (i >> 1) + 8 * (i & 1); };
+
+  floatx4_t acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < K; k0 += BK) {
+    u32x4 x = {0, 0, 0, 0}, y = x;
+    if (k0 + kr < K) {
+      x = load_upto(a.a + (first + k0 + kr) * a.lda + m_at, M - m_at, M);
+      y = load_upto(a.b + (first + k0 + kr) * a.ldb + n_at, N - n_at, N);
+    }
+    if (k0) __syncthreads();
+    *reinterpret_cast<u32x4*>(sA + at) = x;
+    *reinterpret_cast<u32x4*>(sB + at) = y;
+    __syncthreads();
+    frag_t bf[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bf[j] = read_b<DT, ROW>(sB + ((frag_at ^ block(j)) ^ (wn * 64)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const frag_t af = read_b<DT, ROW>(sA + ((frag_at ^ block(i)) ^ (wm * 128)));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma(bf[j], af, acc[i][j]);
+    }
+  }
+  __syncthreads();
+  const bool odd = (g & 1) != 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = wm * 64 + 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + qt, chunk = wn * 4 + g;
+    *reinterpret_cast<u32x4*>(lds + m * 256 + 16 * (chunk ^ (m & 15))) =
+        odd ? pack8<DT>(acc[i][1], acc[i][0]) : pack8<DT>(acc[i][0], acc[i][1]);
+  }
+  __syncthreads();
+  uint16_t* C = a.c + (int64_t)e * M * N;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = kr + 32 * j, m = m0 + r;
+    if (m < M && n_at < N)
+      moe::store_row<moe::kAnyAddress>(C + (int64_t)m * N, n_at, N,
+                                       *reinterpret_cast<const u32x4*>(lds + r * 256 + 16 * ((tid & 15) ^ (r & 15))));
+  }
+}
+
 } // namespace grouped
 } // namespace pgemm

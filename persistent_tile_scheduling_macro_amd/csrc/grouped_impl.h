@@ -15,6 +15,7 @@ kernel_fn pick(int body, bool grad, bool nk) {
     case kFew16: return nk ? grouped_few_kernel<DT, true, 1, 1> : grouped_few_kernel<DT, false, 1, 4>;
     case kFew16Wide: return nk ? grouped_few_kernel<DT, true, 1, 2> : grouped_few_kernel<DT, false, 1, 4>;
     case kFew32Wide: return nk ? grouped_few_kernel<DT, true, 2, 2> : grouped_few_kernel<DT, false, 2, 4>;
+    case kFewGrad: return grad_few_kernel<DT>;
     default:
       return grad ? grouped_kernel<DT, true, false> : nk ? grouped_kernel<DT, false, true> : grouped_kernel<DT, false, false>;
   }

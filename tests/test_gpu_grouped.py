@@ -57,7 +57,8 @@ def check_all(moe, x, w, dy, off, layout, what):
 @pytest.mark.parametrize("counts,K,N", [
     ([1], 1, 1), ([1], 64, 64), ([0, 1, 0], 8, 8), ([3, 0, 2], 7, 5), ([17, 16, 15], 128, 96), ([5, 9, 1, 0, 33], 200, 72),
     ([130, 0, 127, 128], 136, 264), ([64, 65, 63], 65, 129), ([300, 1, 40], 520, 136), ([257, 255, 256, 511], 256, 512),
-    ([700, 300], 1000, 264), ([513, 90], 1001, 257), ([2, 1, 3, 2], 2047, 130), ([9, 7], 2048, 8)])
+    ([700, 300], 1000, 264), ([513, 90], 1001, 257), ([2, 1, 3, 2], 2047, 130), ([9, 7], 2048, 8),
+    ([90, 0, 3, 1], 136, 200), ([0, 0, 70, 0], 257, 131), ([20, 32, 33], 7, 5), ([32], 128, 128), ([31, 33], 264, 6)])
 def test_products_and_gradients(moe, counts, K, N, layout, dtype):
     check_all(moe, *operands(counts, K, N, layout, DT[dtype]), layout, f"{counts} {K}x{N} {layout} {dtype}")
 
