@@ -84,7 +84,12 @@ int pick_rows_body(const grouped::Args& a, bool direct, bool nk) {
 // 32768 rows: 64 x 64 647 us in one piece, 512 x 512 653 us, 2048 x 2048 718 us.)
 struct GradPlan { int body; int64_t pieces; };
 GradPlan plan_grad(int64_t R, int64_t E, int64_t I, int64_t J) {
-  if (R / E <= 32) return {grouped::kFewGrad, 1};
+  // The body for few rows, where its many small steps were faster (us, against the better of the others): 32
+  // experts, 2048 x 1536, of 31 rows 39, 64 rows 47 (58), 94 rows 63 (64), 128 rows 77 (75); eight of 200 rows, 1024 x
+  // 1024 12 (16), 1023 x 1023 17 (15); one of 400 rows, 512 x 512 9 (18).
+  const int64_t tiles_128 = E * ((I + 127) / 128) * ((J + 127) / 128), rows = R / E;
+  if (rows <= 96 || (rows <= 256 && tiles_128 <= 768 && I % 8 == 0 && J % 8 == 0) || (rows <= 512 && tiles_128 <= 128))
+    return {grouped::kFewGrad, 1};
   GradPlan best = {grouped::kAnyAlignment, 1};
   double least = 1e30;
   const double mean = (double)R / E;
