@@ -407,7 +407,8 @@ int pgemm_read_work_counter(pgemm_handle_t h, int32_t* value);
  * allocated. Entries of pos outside [0, n) count as dropped.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
  * k < 1, E < 1, an unknown type or too small a workspace;
- * PGEMM_ERR_UNSUPPORTED for n or H above 2^30 or E above 1024. */
+ * PGEMM_ERR_UNSUPPORTED for n or H above 2^30, E above 1024, or more tokens than
+ * one launch takes (2^26 of up to 1024 elements, 2^24 of more). */
 
 /* Integer type of the expert ids. */
 typedef enum { PGEMM_IDS_I32 = 0, PGEMM_IDS_I64 = 1 } pgemm_ids_t;
@@ -453,7 +454,7 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
  * addresses are the fastest. Nothing is allocated.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
  * E < 1, an unknown layout or type; PGEMM_ERR_UNSUPPORTED for sizes above
- * 2^30, E above 1024 or 2^31 output tiles. */
+ * 2^30, E above 1024 or more output tiles than one launch takes (2^23). */
 
 /* Enqueue y[r] = x[r] * w[e(r)]. x: R rows of K; w: [E, K, N] for PGEMM_B_KN,
  * [E, N, K] for PGEMM_B_NK; y: [R, N], zeros in rows of no expert (whatever x
@@ -503,7 +504,8 @@ typedef enum { PGEMM_W4_INT4 = 0, PGEMM_W4_E2M1 = 1 } pgemm_w4_format_t;
  * allocated; pointers may have any alignment their elements have.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
  * an unknown group, format or type, zeros with E2M1, or E > 1 without
- * offsets; PGEMM_ERR_UNSUPPORTED for sizes above 2^30 or E above 65534. */
+ * offsets; PGEMM_ERR_UNSUPPORTED for sizes above 2^30, E above 65534 or N above
+ * what one launch takes (2^27). */
 int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, const void* scales, const void* zeros,
                  const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int64_t E, int group, int fmt,
                  int dtype);

@@ -9,6 +9,7 @@ HIP library has not been built, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +58,19 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m persistent_tile_scheduling_macro_amd.build` (hipcc, gfx950)")
 
+
+
+def _load_hip_runtime() -> None:
+    """Load torch's own HIP runtime before the library asks for one, whichever of the two is imported first: a process
+    that holds both it and the system's passes streams of one to the other."""
+    torch = importlib.util.find_spec("torch")
+    if torch is not None and torch.origin:
+        path = os.path.join(os.path.dirname(torch.origin), "lib", "libamdhip64.so")
+        if os.path.exists(path):
+            ctypes.CDLL(path)
+
+
+_load_hip_runtime()
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i64, _i32, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
 _ip = ctypes.POINTER(ctypes.c_int)

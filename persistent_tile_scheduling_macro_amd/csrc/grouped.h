@@ -35,6 +35,7 @@ struct Args {
   int N;    // columns of c
   int K;    // rows form: length of the sum (the gradient form has an expert's number of rows)
   int n_n;  // tiles along N
+  int most_tiles; // no ascending bounds give more tiles
   int split;   // gradient form: pieces an expert's rows are cut into
   float* part; // split > 1: their sums, [E][split][M][N rounded up to 8]
 };

@@ -122,8 +122,11 @@ int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool
   a.n_n = (a.N + t.bn - 1) / t.bn;
   int64_t grid = tile_rows(t.bm) * a.n_n;
   if (grid > INT32_MAX - 8) return fail(h, PGEMM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+  a.most_tiles = (int)grid;
   if (body == grouped::kPingPong) grid = grid < h->cus ? grid : h->cus; // persistent, one workgroup a CU
   else if (!grad) grid = (grid + 7) / 8 * 8;
+  if (grid * t.threads > UINT32_MAX) // threads of a launch
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "%lld output tiles are more than one launch takes", (long long)grid);
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
   const bool f16 = dtype == PGEMM_F16;

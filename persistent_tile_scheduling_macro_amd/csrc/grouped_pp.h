@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(512, 2) grouped_pp_kernel(Args a) {
       }
     }
     __syncthreads();
-    T = __builtin_amdgcn_readfirstlane(s_tiles[a.E]);
+    T = min(__builtin_amdgcn_readfirstlane(s_tiles[a.E]), a.most_tiles); // bounds that run backwards stay finite
   }
   if ((int)blockIdx.x >= T) return;
 

@@ -11,6 +11,13 @@ constexpr int64_t kSmallSlots = 2048;
 // Workgroups that clear the rows of dropped slots (they leave at once if there are none).
 constexpr int kClearBlocks = 128;
 
+// One wave carries a row of up to 1024 elements (two passes of 16 bytes a lane), four waves a longer one.
+int lanes_of(int64_t H) { return H > 1024 ? 256 : 64; }
+unsigned token_blocks(int64_t T, int64_t H) {
+  const int64_t per = moe::kThreads / lanes_of(H);
+  return (unsigned)((T + per - 1) / per);
+}
+
 int check_rows(pgemm_ctx* h, int64_t T, int64_t k, int64_t H, int dtype) {
   if (T < 0 || k < 1 || H < 0)
     return fail(h, PGEMM_ERR_INVALID_ARG, "sizes T=%lld k=%lld H=%lld", (long long)T, (long long)k, (long long)H);
@@ -18,6 +25,8 @@ int check_rows(pgemm_ctx* h, int64_t T, int64_t k, int64_t H, int dtype) {
     return fail(h, PGEMM_ERR_UNSUPPORTED, "T * k and H must not exceed 2^30");
   if (dtype != PGEMM_F16 && dtype != PGEMM_BF16)
     return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
+  if (((int64_t)token_blocks(T, H) + kClearBlocks) * moe::kThreads > UINT32_MAX) // threads of a launch
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "T=%lld tokens of H=%lld are more than one launch takes", (long long)T, (long long)H);
   return PGEMM_OK;
 }
 
@@ -40,13 +49,6 @@ bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
 int64_t sort_chunk(int64_t n) {
   const int64_t tiles = (n + moe::kTile - 1) / moe::kTile;
   return (tiles + moe::kMaxChunks - 1) / moe::kMaxChunks * moe::kTile;
-}
-
-// One wave carries a row of up to 1024 elements (two passes of 16 bytes a lane), four waves a longer one.
-int lanes_of(int64_t H) { return H > 1024 ? 256 : 64; }
-unsigned token_blocks(int64_t T, int64_t H) {
-  const int64_t per = moe::kThreads / lanes_of(H);
-  return (unsigned)((T + per - 1) / per);
 }
 
 template <class ID>

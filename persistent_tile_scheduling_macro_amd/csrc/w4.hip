@@ -53,6 +53,8 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   const int cb = experts * ((N + 31) / 32) >= 2 * h->cus ? 2 : 1;
   const int64_t row_groups = offsets ? E + 1 : (M + rows - 1) / rows;
   const int64_t cols = (N + 16 * cb - 1) / (16 * cb);
+  if (cols * w4::waves_of(rows) * 64 > UINT32_MAX) // threads of a launch
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "N=%lld columns are more than one launch takes", (long long)N);
   const int form = zeros ? w4::kInt4Zero : fmt == PGEMM_W4_E2M1 ? w4::kE2M1 : w4::kInt4;
   const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, rows, cb) : w4::pick_bf16(form, group, rows, cb);
   if (row_groups <= 65535) {

@@ -36,7 +36,7 @@ def test_routing(env):
     for kw in ({"T": -1}, {"k": 0}, {"H": -1}, {"E": 0}, {"dt": F8}, {"it": 2}, {"ldx": -1}, {"x": None}, {"ids": None},
                {"off": None}, {"order": None}, {"pos": None}, {"xs": None}, {"T": 40000}, {"T": 40000, "work": b, "wb": 8}):
         refused(pg, bad, lambda kw=kw: dispatch(**kw))
-    for kw in ({"E": 1025}, {"T": BIG}, {"H": BIG}, {"T": 2 ** 29, "k": 3}):
+    for kw in ({"E": 1025}, {"T": BIG}, {"H": BIG}, {"T": 2 ** 29, "k": 3}, {"T": 2 ** 27, "k": 1}):
         refused(pg, no, lambda kw=kw: dispatch(**kw))
     for kw in ((-1, 2, 8, F16), (2, 0, 8, F16), (2, 2, -1, F16), (2, 2, 8, F8)):
         T, k, H, dt = kw
@@ -86,7 +86,7 @@ def test_4_bit_product(env):
     for kw in ({"M": -1}, {"N": -1}, {"K": -1}, {"E": 0}, {"ldx": -1}, {"group": 48}, {"fmt": 2}, {"dt": F8}, {"fmt": 1, "z": b},
                {"E": 2}, {"x": None}, {"q": None}, {"s": None}, {"y": None}):
         refused(pg, bad, lambda kw=kw: run(**kw))
-    for kw in ({"M": BIG}, {"N": BIG}, {"K": BIG}, {"E": 65535, "off": b}):
+    for kw in ({"M": BIG}, {"N": BIG}, {"K": BIG}, {"E": 65535, "off": b}, {"N": 2 ** 29}):
         refused(pg, no, lambda kw=kw: run(**kw))
 
 
