@@ -87,8 +87,11 @@ GradPlan plan_grad(int64_t R, int64_t E, int64_t I, int64_t J) {
   // The body for few rows, where its many small steps were faster (us, against the better of the others): 32
   // experts, 2048 x 1536, of 31 rows 39, 64 rows 47 (58), 94 rows 63 (64), 128 rows 77 (75); eight of 200 rows, 1024 x
   // 1024 12 (16), 1023 x 1023 17 (15); one of 400 rows, 512 x 512 9 (18).
+  // Odd sizes, whose edges it moves inside the loop, only with few rows or very few tiles: ten of 480 rows, 144 x 1184
+  // 22 (25), 145 x 1183 34 (24).
   const int64_t tiles_128 = E * ((I + 127) / 128) * ((J + 127) / 128), rows = R / E;
-  if (rows <= 96 || (rows <= 256 && tiles_128 <= 768 && I % 8 == 0 && J % 8 == 0) || (rows <= 512 && tiles_128 <= 128))
+  const bool even = I % 8 == 0 && J % 8 == 0;
+  if (rows <= 96 || (even && rows <= 256 && tiles_128 <= 768) || (rows <= 512 && tiles_128 <= (even ? 256 : 32)))
     return {grouped::kFewGrad, 1};
   GradPlan best = {grouped::kAnyAlignment, 1};
   double least = 1e30;
