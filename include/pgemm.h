@@ -449,8 +449,8 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
  * The host never reads them, so a call can be captured and replayed with
  * other bounds. dtype is PGEMM_F16 or PGEMM_BF16; ld* is the distance of two
  * rows in elements (0 repeats one row), w and the outputs are contiguous.
- * Sums are fp32, rounded once, and the same on every run. Sizes and addresses
- * may be odd; K and N of a multiple of 8 elements with rows at 16-byte
+ * Sums are fp32, rounded once, and the same on every run. Sizes may be odd, and
+ * addresses any that elements have; K and N of a multiple of 8 with rows at 16-byte
  * addresses are the fastest. Nothing is allocated.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
  * E < 1, an unknown layout or type; PGEMM_ERR_UNSUPPORTED for sizes above
@@ -486,7 +486,7 @@ int pgemm_grouped_weight_grad_workspace(int64_t R, int64_t E, int64_t I, int64_t
 typedef enum { PGEMM_W4_INT4 = 0, PGEMM_W4_E2M1 = 1 } pgemm_w4_format_t;
 
 /* Enqueue y = x * dec(q)^T on the handle's stream, for the few rows of a
- * decoding batch (any number is computed; each 64 read the weights again).
+ * decoding batch (any number is computed; each 32 read the weights again).
  *   x: M rows of K elements, ldx apart (0 repeats one row); y: [M, N].
  *   q: [E, N, ceil(K / 2)] bytes, code k of a row in byte k / 2, the even one
  *     in the low nibble; a last half byte is ignored.
