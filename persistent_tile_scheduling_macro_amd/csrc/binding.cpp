@@ -4,9 +4,11 @@
 // on torch's current stream: what a call of a few microseconds on the GPU can
 // afford on the host (a combine of 16 tokens took 10.7 us of Python). No
 // arithmetic happens here. Shapes that do not belong together raise
-// ValueError, wrong types TypeError, a refusal of the library PgemmError.
+// ValueError, wrong types TypeError, a refusal of the library PgemmError, a
+// forward-mode tangent NotImplementedError.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -44,9 +46,18 @@ int dtype_of(const Tensor& t, const char* name) {
   type(join({name, " is ", c10::toString(t.scalar_type()), ", not float16 or bfloat16"}));
 }
 
+// A tangent of t would be lost: the kernels read values only. (Inside an autograd function torch has turned
+// forward mode off and refuses the tangent itself.)
+void no_tangent(const Tensor& t, const char* name) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode() || !t._fw_grad(0).defined()) return;
+  PyErr_SetString(PyExc_NotImplementedError, join({name, " carries a tangent: forward-mode derivatives are not implemented"}).c_str());
+  throw py::error_already_set();
+}
+
 // A 2-D fp16/bf16 tensor whose rows are contiguous (a copy of one whose are not).
 Tensor rows_of(const Tensor& t, const char* name) {
   dtype_of(t, name);
+  no_tangent(t, name);
   if (t.dim() != 2) value(join({name, " has shape ", shape(t), ", not two dimensions"}));
   // a negative stride cannot occur in torch; one that repeats a row (0) is fine
   return t.stride(1) == 1 || t.size(1) <= 1 ? t : t.contiguous();
@@ -180,6 +191,7 @@ std::pair<Tensor, Tensor> check_combine(const char* name, const Tensor& ys_, con
   Tensor ys = rows_of(ys_, "ys");
   if (ys.size(0) != p.n) value(join({name, ": ys has ", num(ys.size(0)), " rows, the plan ", num(p.n)}));
   if (w.scalar_type() != at::kFloat) type(join({name, ": weights are ", c10::toString(w.scalar_type()), ", not float32"}));
+  no_tangent(w, "weights");
   if (w.dim() != 2 || w.size(0) != p.T || w.size(1) != p.k)
     value(join({name, ": weights have shape ", shape(w), ", not [", num(p.T), ", ", num(p.k), "]"}));
   return {ys, w.contiguous()};
@@ -226,6 +238,7 @@ Grouped check_grouped(const char* name, const Tensor& x_, const Tensor& w, const
   const Tensor x = rows_of(x_, "x");
   if (w.scalar_type() != x.scalar_type())
     type(join({name, ": w is ", c10::toString(w.scalar_type()), ", x ", c10::toString(x.scalar_type())}));
+  no_tangent(w, "w");
   const int64_t K = x.size(1);
   if (w.dim() != 3 || w.size(0) < 1 || w.size(nk ? 2 : 1) != K)
     value(join({name, ": w has shape ", shape(w), " for rows of ", num(K), " and layout ", nk ? "'nk'" : "'kn'"}));
@@ -252,8 +265,8 @@ Tensor grouped(const Tensor& x, const Tensor& w, const Tensor& offsets, bool nk)
 std::tuple<c10::optional<Tensor>, c10::optional<Tensor>> grouped_backward(const Tensor& dy_, const Tensor& x, const Tensor& w,
                                                                           const Tensor& offsets, bool nk, bool need_dx,
                                                                           bool need_dw) {
-  const Grouped g = check_grouped("grouped_matmul_backward", x, w, offsets, nk);
   const Tensor dy = rows_of(dy_, "dy");
+  const Grouped g = check_grouped("grouped_matmul_backward", x, w, offsets, nk);
   if (dy.size(0) != g.R || dy.size(1) != g.N)
     value(join({"dy has shape ", shape(dy), ", not [", num(g.R), ", ", num(g.N), "]"}));
   if (dy.scalar_type() != g.x.scalar_type())
@@ -286,6 +299,7 @@ Tensor w4(const Tensor& x_, const Tensor& q_, const Tensor& scales_, const c10::
   if (q_.scalar_type() != at::kByte) type(join({"q is ", c10::toString(q_.scalar_type()), ", not uint8"}));
   if (scales_.scalar_type() != x.scalar_type())
     type(join({"scales are ", c10::toString(scales_.scalar_type()), ", x ", c10::toString(x.scalar_type())}));
+  no_tangent(scales_, "scales");
   const int lead = offsets_ ? 1 : 0;
   if (q_.dim() != lead + 2 || q_.size(-1) != (K + 1) / 2)
     value(join({"q has shape ", shape(q_), " for K = ", num(K), offsets_ ? " and offsets" : ""}));

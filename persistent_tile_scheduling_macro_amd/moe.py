@@ -12,8 +12,8 @@ waiting. Rows are fp16 or bf16, sums fp32 rounded once.
 
 The functions are differentiable: where torch records gradients they enter its graph, and each gradient is
 also a function of its own (``*_backward``), which is what to capture into a HIP graph. Tensors of the wrong shape
-raise ValueError, of the wrong type TypeError, a refusal of the library raises PgemmError. A tensor whose rows are not
-contiguous is copied first.
+raise ValueError, of the wrong type TypeError, a refusal of the library raises PgemmError, a tensor that carries a
+forward-mode tangent NotImplementedError. A tensor whose rows are not contiguous is copied first.
 """
 from __future__ import annotations
 
