@@ -19,10 +19,10 @@ def matmul(x, q, scales, zeros=None, *, group: int, fmt: str = "int4", offsets=N
     [N, ceil(K/group)], group 32, 64 or 128. fmt "int4": (code - zero) * scale, zeros uint8 like scales (their low
     four bits), or None for 8; fmt "e2m1": the OCP 4-bit float times scale. With offsets int32 [E+1] on the device
     q, scales and zeros have a leading E, and matrix e takes x's rows offsets[e]..offsets[e+1]-1; other rows give
-    zeros. For serving: it records no gradient, and refuses an x that wants one.
+    zeros. For serving: it records no gradient, and refuses an x or scales that want one.
     """
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("w4.matmul has no gradient: call it under torch.no_grad() or on a detached x")
+    if (x.requires_grad or scales.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("w4.matmul has no gradient: call it under torch.no_grad() or on detached x and scales")
     if fmt not in _FORMATS:
         raise ValueError(f"fmt {fmt!r} is not one of {sorted(_FORMATS)}")
     return _ops.w4(x, q, scales, zeros, group, _FORMATS[fmt], offsets)

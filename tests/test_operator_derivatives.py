@@ -38,3 +38,11 @@ def test_tangents_are_refused(shapes, call, which):
             call(*args)
         with torch.no_grad(), pytest.raises(NotImplementedError, match="tangent"):  # which is about reverse mode only
             call(*args)
+
+
+def test_scales_that_want_a_gradient_are_refused():
+    q, s = t(8, 32, dtype=U8), t(8, 2).requires_grad_(True)
+    with pytest.raises(ValueError, match="no gradient"):
+        w4.matmul(t(4, 64), q, s, group=32)
+    with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):  # none is recorded: on to the next check
+        w4.matmul(t(4, 64), q, s, group=32)
