@@ -60,14 +60,15 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, ids, num_experts):
         xs, *plan = _ops.dispatch(x, ids, num_experts)
-        ctx.plan, ctx.k = plan, ids.shape[1]
+        ctx.save_for_backward(*plan)
+        ctx.k = ids.shape[1]
         ctx.mark_non_differentiable(*plan)
         return xs, *plan
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs, *_):
-        return _ops.dispatch_backward(dxs, *ctx.plan, ctx.k), None, None
+        return _ops.dispatch_backward(dxs, *ctx.saved_tensors, ctx.k), None, None
 
 
 # ----------------------------------------------------------------- combine

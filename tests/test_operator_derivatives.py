@@ -46,3 +46,39 @@ def test_scales_that_want_a_gradient_are_refused():
         w4.matmul(t(4, 64), q, s, group=32)
     with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):  # none is recorded: on to the next check
         w4.matmul(t(4, 64), q, s, group=32)
+
+
+class HostDispatch:
+    """The two bindings that moe.dispatch's autograd node calls, for one expert and two slots a token."""
+
+    @staticmethod
+    def dispatch(x, ids, E):
+        n = 2 * x.shape[0]
+        return x.repeat_interleave(2, 0), torch.tensor([0, n], dtype=I32), torch.arange(n, dtype=I32), torch.arange(n, dtype=I32)
+
+    @staticmethod
+    def dispatch_backward(dxs, offsets, order, pos, k):
+        return dxs.view(-1, k, dxs.shape[1]).sum(1)
+
+
+def test_a_plan_changed_before_the_backward_pass_is_noticed(monkeypatch):
+    monkeypatch.setattr(moe, "_ops", HostDispatch)
+    x = torch.ones(4, 8, dtype=F16, requires_grad=True)
+    xs, route = moe.dispatch(x, t(4, 2, dtype=I32), 1)
+    xs.sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2))
+    for name in ("offsets", "order", "pos"):
+        xs, route = moe.dispatch(x, t(4, 2, dtype=I32), 1)
+        getattr(route, name).fill_(0)
+        with pytest.raises(RuntimeError, match="inplace"):
+            xs.sum().backward()
+
+
+def test_saved_tensor_hooks_see_the_plan(monkeypatch):
+    monkeypatch.setattr(moe, "_ops", HostDispatch)
+    x = torch.ones(4, 8, dtype=F16, requires_grad=True)
+    packed = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda s: packed.append(s.shape) or s, lambda s: s):
+        xs, _ = moe.dispatch(x, t(4, 2, dtype=I32), 1)
+    assert sorted(packed) == [(2,), (8,), (8,)]
+    xs.sum().backward()
