@@ -10,6 +10,7 @@
 
 #include "../../include/pgemm.h"
 #include "kernels.h"
+#include "launch.h"
 
 struct pgemm_ctx {
   int device = 0;
@@ -77,9 +78,8 @@ class DeviceScope {
   bool ok_ = false;
 };
 
-// Status of the launches made since the last call, as a pgemm_status_t.
-inline int launch_status(pgemm_ctx* h, const char* what) {
-  const hipError_t e = hipGetLastError();
+// Status of a call's launches (the first that failed), as a pgemm_status_t.
+inline int launch_status(pgemm_ctx* h, hipError_t e, const char* what) {
   return e == hipSuccess ? PGEMM_OK : fail(h, PGEMM_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 

@@ -133,15 +133,15 @@ int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
   const bool f16 = dtype == PGEMM_F16;
-  hipLaunchKernelGGL(f16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk), dim3((unsigned)grid),
-                     dim3(t.threads), 0, h->stream, a);
-  if (a.split > 1) {
+  hipError_t e = enqueue(h->stream, dim3((unsigned)grid), dim3(t.threads),
+                         f16 ? grouped::pick_f16(body, grad, nk) : grouped::pick_bf16(body, grad, nk), a);
+  if (e == hipSuccess && a.split > 1) {
     const bool shared = a.split >= 8;
     const int64_t sums = (int64_t)a.E * a.M * ((a.N + 7) / 8), per = shared ? 32 : 256;
-    hipLaunchKernelGGL(f16 ? grouped::join_f16(shared) : grouped::join_bf16(shared), dim3((unsigned)((sums + per - 1) / per)),
-                       dim3(256), 0, h->stream, a);
+    e = enqueue(h->stream, dim3((unsigned)((sums + per - 1) / per)), dim3(256),
+                f16 ? grouped::join_f16(shared) : grouped::join_bf16(shared), a);
   }
-  return launch_status(h, "grouped product");
+  return launch_status(h, e, "grouped product");
 }
 
 // Row strides up to which a tile's 32-bit offsets reach its last row (256 rows of 2-byte elements below 2^31).

@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch.h"
+
 namespace pgemm {
 
 __global__ void __launch_bounds__(64) hold_cu_kernel(uint64_t ticks) {
@@ -27,8 +29,8 @@ __global__ void __launch_bounds__(64) hold_cu_kernel(uint64_t ticks) {
   }
 }
 
-void launch_hold(int n, uint64_t ticks, hipStream_t stream) {
-  hipLaunchKernelGGL(hold_cu_kernel, dim3(n), dim3(64), 0, stream, ticks);
+hipError_t launch_hold(int n, uint64_t ticks, hipStream_t stream) {
+  return enqueue(stream, dim3(n), dim3(64), hold_cu_kernel, ticks);
 }
 
 } // namespace pgemm

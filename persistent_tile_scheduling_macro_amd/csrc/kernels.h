@@ -41,10 +41,10 @@ kernel_fn pick_fixup_bf16(int body);
 kernel_fn pick_fixup_f8(int body);
 
 // K == 0: C = 0 (an empty sum), rows x cols elements with rows ldc elements apart.
-void launch_fill_zero(void* C, int64_t rows, int64_t cols, int64_t ldc, hipStream_t stream);
+hipError_t launch_fill_zero(void* C, int64_t rows, int64_t cols, int64_t ldc, hipStream_t stream);
 
 // Benchmark aid (hold.hip): n workgroups that each hold a whole CU's LDS
 // until the constant-rate clock has advanced by `ticks`.
-void launch_hold(int n, uint64_t ticks, hipStream_t stream);
+hipError_t launch_hold(int n, uint64_t ticks, hipStream_t stream);
 
 } // namespace pgemm

@@ -52,36 +52,35 @@ int64_t sort_chunk(int64_t n) {
 }
 
 template <class ID>
-void launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, int access) {
+hipError_t launch_dispatch(pgemm_ctx* h, const moe::SortArgs& s, moe::MoveArgs a, int access) {
   const hipStream_t st = h->stream;
   if (s.n <= kSmallSlots) {
     auto kern = access ? moe::dispatch_small_kernel<ID, moe::kAligned> : moe::dispatch_small_kernel<ID, moe::kAnyAddress>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)a.T + 1), dim3(moe::kThreads), 0, st, s, a);
-    return;
+    return enqueue(st, dim3((unsigned)a.T + 1), dim3(moe::kThreads), kern, s, a);
   }
   const int chunks = (int)((s.n + s.chunk - 1) / s.chunk);
-  hipLaunchKernelGGL(moe::sort_count_kernel<ID>, dim3(chunks), dim3(moe::kThreads), 0, st, s);
-  hipLaunchKernelGGL(moe::sort_place_kernel<ID>, dim3(chunks), dim3(moe::kThreads), 0, st, s, chunks);
-  if (a.H == 0) return;
+  hipError_t e = enqueue(st, dim3(chunks), dim3(moe::kThreads), moe::sort_count_kernel<ID>, s);
+  if (e == hipSuccess) e = enqueue(st, dim3(chunks), dim3(moe::kThreads), moe::sort_place_kernel<ID>, s, chunks);
+  if (e != hipSuccess || a.H == 0) return e;
   a.token_blocks = (int)token_blocks(a.T, a.H);
   const dim3 grid((unsigned)a.token_blocks + kClearBlocks);
   const bool wide = lanes_of(a.H) == 256;
   auto kern = access == moe::kStream    ? moe::move_kernel<moe::kStream, 256>
               : access == moe::kAligned ? (wide ? moe::move_kernel<moe::kAligned, 256> : moe::move_kernel<moe::kAligned, 64>)
                                         : (wide ? moe::move_kernel<moe::kAnyAddress, 256> : moe::move_kernel<moe::kAnyAddress, 64>);
-  hipLaunchKernelGGL(kern, grid, dim3(moe::kThreads), 0, st, a);
+  return enqueue(st, grid, dim3(moe::kThreads), kern, a);
 }
 
 template <int DT, int AL, int LANES, bool WEIGHTED>
-void launch_sum_k(pgemm_ctx* h, const moe::SumArgs& a, unsigned grid) {
+hipError_t launch_sum_k(pgemm_ctx* h, const moe::SumArgs& a, unsigned grid) {
   auto kern = a.k >= 8   ? moe::gather_sum_kernel<DT, AL, LANES, 8, WEIGHTED>
               : a.k >= 3 ? moe::gather_sum_kernel<DT, AL, LANES, 4, WEIGHTED>
                          : moe::gather_sum_kernel<DT, AL, LANES, 2, WEIGHTED>;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
+  return enqueue(h->stream, dim3(grid), dim3(moe::kThreads), kern, a);
 }
 
 template <int DT, bool WEIGHTED>
-void launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int access) {
+hipError_t launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int access) {
   const unsigned grid = token_blocks(a.T, a.H);
   const bool wide = lanes_of(a.H) == 256;
   if (access == moe::kStream) return launch_sum_k<DT, moe::kStream, 256, WEIGHTED>(h, a, grid);
@@ -92,15 +91,15 @@ void launch_sum(pgemm_ctx* h, const moe::SumArgs& a, int access) {
 }
 
 template <int DT, int AL, int LANES>
-void launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
+hipError_t launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
   auto kern = a.k >= 8   ? moe::combine_backward_kernel<DT, AL, LANES, 8>
               : a.k >= 3 ? moe::combine_backward_kernel<DT, AL, LANES, 4>
                          : moe::combine_backward_kernel<DT, AL, LANES, 2>;
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(moe::kThreads), 0, h->stream, a);
+  return enqueue(h->stream, dim3(grid), dim3(moe::kThreads), kern, a);
 }
 
 template <int DT>
-void launch_back(pgemm_ctx* h, const moe::BackArgs& a, int access) {
+hipError_t launch_back(pgemm_ctx* h, const moe::BackArgs& a, int access) {
   const unsigned grid = (unsigned)a.token_blocks + kClearBlocks;
   const bool wide = lanes_of(a.H) == 256;
   if (access == moe::kStream) return launch_back_k<DT, moe::kStream, 256>(h, a, grid);
@@ -132,9 +131,11 @@ int sum_impl(pgemm_handle_t h, const void* rows, int64_t ld, const float* w, con
   a.n = (int)(T * k);
   const bool al = H % 8 == 0 && ld % 8 == 0 && aligned16(rows) && aligned16(out);
   const int access = access_of(al, T * k, H);
-  if (dtype == PGEMM_BF16) weighted ? launch_sum<kBF16, true>(h, a, access) : launch_sum<kBF16, false>(h, a, access);
-  else weighted ? launch_sum<kF16, true>(h, a, access) : launch_sum<kF16, false>(h, a, access);
-  return launch_status(h, weighted ? "combine" : "dispatch backward");
+  const bool bf16 = dtype == PGEMM_BF16;
+  if (weighted)
+    return launch_status(h, bf16 ? launch_sum<kBF16, true>(h, a, access) : launch_sum<kF16, true>(h, a, access), "combine");
+  return launch_status(h, bf16 ? launch_sum<kBF16, false>(h, a, access) : launch_sum<kF16, false>(h, a, access),
+                       "dispatch backward");
 }
 
 } // namespace
@@ -197,9 +198,8 @@ int pgemm_moe_dispatch(pgemm_handle_t h, const void* x, int64_t ldx, const void*
   a.token_blocks = 0;
   const bool al = H % 8 == 0 && ldx % 8 == 0 && aligned16(x) && aligned16(xs);
   const int access = access_of(al, T * k, H);
-  if (ids_type == PGEMM_IDS_I32) launch_dispatch<int32_t>(h, s, a, access);
-  else launch_dispatch<int64_t>(h, s, a, access);
-  return launch_status(h, "dispatch");
+  const bool i32 = ids_type == PGEMM_IDS_I32;
+  return launch_status(h, i32 ? launch_dispatch<int32_t>(h, s, a, access) : launch_dispatch<int64_t>(h, s, a, access), "dispatch");
 }
 
 int pgemm_moe_dispatch_backward(pgemm_handle_t h, const void* dxs, int64_t lddxs, const int32_t* pos, int64_t T,
@@ -245,9 +245,8 @@ int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddou
   a.token_blocks = (int)token_blocks(T, H);
   const bool al = H % 8 == 0 && lddout % 8 == 0 && ldys % 8 == 0 && aligned16(dout) && aligned16(ys) && aligned16(dys);
   const int access = access_of(al, T * k, H);
-  if (dtype == PGEMM_BF16) launch_back<kBF16>(h, a, access);
-  else launch_back<kF16>(h, a, access);
-  return launch_status(h, "combine backward");
+  return launch_status(h, dtype == PGEMM_BF16 ? launch_back<kBF16>(h, a, access) : launch_back<kF16>(h, a, access),
+                       "combine backward");
 }
 
 } // extern "C"

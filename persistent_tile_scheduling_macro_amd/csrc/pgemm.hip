@@ -353,9 +353,7 @@ int run_impl(pgemm_handle_t h, const void* A, int64_t lda, const void* B, int64_
                 (long long)lda, (long long)ldb, (long long)ldc);
   if (hipSetDevice(h->device) != hipSuccess) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
   if (K == 0) {
-    launch_fill_zero(C, M, N, ldc, h->stream);
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? PGEMM_OK : fail(h, PGEMM_ERR_HIP, "zero-fill launch: %s", hipGetErrorString(e));
+    return launch_status(h, launch_fill_zero(C, M, N, ldc, h->stream), "zero-fill");
   }
   if (!A || !B) return fail(h, PGEMM_ERR_INVALID_ARG, "A or B is NULL");
   const int64_t per16 = 16 / esize_of(dtype); // elements per 16 bytes
@@ -432,10 +430,7 @@ int run_impl(pgemm_handle_t h, const void* A, int64_t lda, const void* B, int64_
   }
   if (sched_mode != kStreamK || !pl.fast) {
     kernel_fn k = pick_kernel(dtype, sched_mode, pl.body, p.trace != nullptr, p.b_nk != 0);
-    hipLaunchKernelGGL(k, dim3((unsigned)pl.G), dim3(pl.threads), 0, h->stream, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(h, PGEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
-    return PGEMM_OK;
+    return launch_status(h, enqueue(h->stream, dim3((unsigned)pl.G), dim3(pl.threads), k, p), "kernel");
   }
   // Stream-K as up to three launches on the stream: (1) the W whole waves, by
   // the static kernel over the first W*G tiles of the tile order (its tile
@@ -451,26 +446,23 @@ int run_impl(pgemm_handle_t h, const void* A, int64_t lda, const void* B, int64_
     pd.T = (int)(pl.T - pl.sk_tiles); // W * G
     pd.sk_waves = pd.sk_tiles = pd.sk_groups = 0;
     pd.work = nullptr;
-    hipLaunchKernelGGL(pick_kernel(dtype, kStatic, pl.body, p.trace != nullptr, p.b_nk != 0), dim3((unsigned)pl.G),
-                       dim3(pl.threads), 0, h->stream, pd);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(h, PGEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    const hipError_t e = enqueue(h->stream, dim3((unsigned)pl.G), dim3(pl.threads),
+                                 pick_kernel(dtype, kStatic, pl.body, p.trace != nullptr, p.b_nk != 0), pd);
+    if (e != hipSuccess) return launch_status(h, e, "kernel");
   }
   if (pl.sk_tiles > 0) {
     Params ps = p;
     ps.sk_waves = 0;
     ps.G = pl.sk_groups;
-    hipLaunchKernelGGL(pick_kernel(dtype, kStreamK, pl.body, p.trace != nullptr, p.b_nk != 0),
-                       dim3((unsigned)pl.sk_groups), dim3(pl.threads), 0, h->stream, ps);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(h, PGEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    hipError_t e = enqueue(h->stream, dim3((unsigned)pl.sk_groups), dim3(pl.threads),
+                           pick_kernel(dtype, kStreamK, pl.body, p.trace != nullptr, p.b_nk != 0), ps);
+    if (e != hipSuccess) return launch_status(h, e, "kernel");
     if (pl.sk_split) {
       // 256 threads cover 8 columns each: 256 / (bn / 8) rows per workgroup
       const unsigned rows_per_wg = 256u / (unsigned)(pl.bn / 8);
-      hipLaunchKernelGGL(pick_fixup(dtype, pl.body), dim3((unsigned)pl.sk_tiles, (unsigned)pl.bm / rows_per_wg),
-                         dim3(256), 0, h->stream, ps);
-      e = hipGetLastError();
-      if (e != hipSuccess) return fail(h, PGEMM_ERR_HIP, "fix-up launch: %s", hipGetErrorString(e));
+      e = enqueue(h->stream, dim3((unsigned)pl.sk_tiles, (unsigned)pl.bm / rows_per_wg), dim3(256), pick_fixup(dtype, pl.body),
+                  ps);
+      if (e != hipSuccess) return launch_status(h, e, "fix-up");
     }
   }
   return PGEMM_OK;
@@ -647,8 +639,9 @@ int pgemm_hold_cus(void* hip_stream, int device, int n_cus, int microseconds) {
   if (hipSetDevice(device) != hipSuccess) return PGEMM_ERR_INVALID_ARG;
   int khz = 0; // rate of the s_memrealtime clock
   if (hipDeviceGetAttribute(&khz, hipDeviceAttributeWallClockRate, device) != hipSuccess || khz <= 0) khz = 100000;
-  launch_hold(n_cus, (uint64_t)microseconds * (uint64_t)khz / 1000u, reinterpret_cast<hipStream_t>(hip_stream));
-  return hipGetLastError() == hipSuccess ? PGEMM_OK : PGEMM_ERR_HIP;
+  return launch_hold(n_cus, (uint64_t)microseconds * (uint64_t)khz / 1000u, reinterpret_cast<hipStream_t>(hip_stream)) == hipSuccess
+             ? PGEMM_OK
+             : PGEMM_ERR_HIP;
 }
 
 int pgemm_read_work_counter(pgemm_handle_t h, int32_t* value) {

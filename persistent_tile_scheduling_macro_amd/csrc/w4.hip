@@ -27,8 +27,7 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   DeviceScope dev(h->device);
   if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
   if (K == 0) { // an empty sum
-    launch_fill_zero(y, M, N, N, h->stream);
-    return launch_status(h, "zero-fill");
+    return launch_status(h, launch_fill_zero(y, M, N, N, h->stream), "zero-fill");
   }
   w4::Args a;
   a.x = static_cast<const uint16_t*>(x);
@@ -58,17 +57,18 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   const int form = zeros ? w4::kInt4Zero : fmt == PGEMM_W4_E2M1 ? w4::kE2M1 : w4::kInt4;
   const w4::kernel_fn kern = dtype == PGEMM_F16 ? w4::pick_f16(form, group, rows, cb) : w4::pick_bf16(form, group, rows, cb);
   if (row_groups <= 65535) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::waves_of(rows) * 64), 0, h->stream, a);
-    return launch_status(h, "w4");
+    return launch_status(h, enqueue(h->stream, dim3((unsigned)cols, (unsigned)row_groups), dim3(w4::waves_of(rows) * 64), kern, a),
+                         "w4");
   }
   // more rows than one grid has: launches of at most 65535 row groups each
-  for (int64_t r = 0; r < row_groups; r += 65535) {
+  hipError_t e = hipSuccess;
+  for (int64_t r = 0; e == hipSuccess && r < row_groups; r += 65535) {
     w4::Args b = a;
     const int64_t from = r * rows, count = row_groups - r < 65535 ? row_groups - r : 65535;
     b.x = a.x + from * ldx;
     b.y = a.y + from * N;
     b.M = (int)(M - from < count * rows ? M - from : count * rows);
-    hipLaunchKernelGGL(kern, dim3((unsigned)cols, (unsigned)count), dim3(w4::waves_of(rows) * 64), 0, h->stream, b);
+    e = enqueue(h->stream, dim3((unsigned)cols, (unsigned)count), dim3(w4::waves_of(rows) * 64), kern, b);
   }
-  return launch_status(h, "w4");
+  return launch_status(h, e, "w4");
 }
