@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(waves_of(ROWS) * 64, ROWS == 32 ? 3 : 4) w4_ke
 #pragma unroll
       for (int c = 0; c < CB; ++c) join[(wave * CB * MB + c * MB + b) * 64 + lane] = acc[b][c];
     __syncthreads();
+    const int end = min(m1, m0 + ROWS); // of this pass: with four rows at once the MFMA's other twelve repeat them
     for (int i = tid; i < CB * MB * 64; i += kWaves * 64) {
       floatx4_t v = join[i];
 #pragma unroll
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(waves_of(ROWS) * 64, ROWS == 32 ? 3 : 4) w4_ke
       const int n = n0 + 16 * c + (l & 15), m = m0 + 16 * b + 4 * (l >> 4);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (n < a.N && m + r < m1)
+        if (n < a.N && m + r < end)
           a.y[(int64_t)(m + r) * a.N + n] = __builtin_bit_cast(uint16_t, to_out(v[r], (out_t*)nullptr));
     }
     __syncthreads();
