@@ -437,10 +437,19 @@ int pgemm_moe_combine(pgemm_handle_t h, const void* ys, int64_t ldys, const floa
 
 /* Its gradients: dys[pos[s]] = w[s] * dout[t] (zeros in the rows from
  * offsets[E] on) and dw[s] = <ys[pos[s]], dout[t]> in fp32 (0 for a dropped
- * slot), s = t*k + j. dout: T rows of H; dys: [n, H]; dw: [T, k]. */
+ * slot), s = t*k + j. dout: T rows of H; dys: [n, H]; dw: [T, k]. For a plan as
+ * the sort left it: rows below offsets[E] that no entry of pos names are not
+ * written. */
 int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
                                const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
                                int64_t E, int64_t H, int dtype, void* dys, float* dw);
+
+/* The same for a plan from which slots were taken after the sort, by setting
+ * their pos outside [0, n) (for instance where an expert has more rows than it
+ * may take): zeros too in a row whose slot, by order, has no place any more. */
+int pgemm_moe_combine_backward_plan(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
+                                    const float* w, const int32_t* offsets, const int32_t* order, const int32_t* pos,
+                                    int64_t T, int64_t k, int64_t E, int64_t H, int dtype, void* dys, float* dw);
 
 /* ---- products of rows sorted by expert ---------------------------------- */
 /*

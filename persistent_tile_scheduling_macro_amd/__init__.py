@@ -114,6 +114,8 @@ _moe_dispatch_backward = _sig("pgemm_moe_dispatch_backward", _int, _vp, _vp, _i6
 _moe_combine = _sig("pgemm_moe_combine", _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp)
 _moe_combine_backward = _sig("pgemm_moe_combine_backward", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
                              _i64, _i64, _int, _vp, _vp)
+_moe_combine_backward_plan = _sig("pgemm_moe_combine_backward_plan", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                                  _i64, _i64, _i64, _int, _vp, _vp)
 _grouped_run = _sig("pgemm_grouped_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int)
 _grouped_weight_grad = _sig("pgemm_grouped_weight_grad", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
                             _i64, _int, _vp, _i64)
@@ -323,6 +325,13 @@ def pgemm_moe_combine_backward(h, dout, lddout: int, ys, ldys: int, w, offsets, 
                                dtype: int, dys, dw) -> None:
     _check(_moe_combine_backward(h, _ptr(dout), lddout, _ptr(ys), ldys, _ptr(w), _ptr(offsets), _ptr(pos), T, k, E, H,
                                  dtype, _ptr(dys), _ptr(dw)), h)
+
+
+def pgemm_moe_combine_backward_plan(h, dout, lddout: int, ys, ldys: int, w, offsets, order, pos, T: int, k: int, E: int,
+                                    H: int, dtype: int, dys, dw) -> None:
+    """The same where slots were taken out of the plan after the sort."""
+    _check(_moe_combine_backward_plan(h, _ptr(dout), lddout, _ptr(ys), ldys, _ptr(w), _ptr(offsets), _ptr(order), _ptr(pos),
+                                      T, k, E, H, dtype, _ptr(dys), _ptr(dw)), h)
 
 
 def pgemm_grouped_run(h, x, ldx: int, w, offsets, y, R: int, E: int, K: int, N: int, layout: int, dtype: int) -> None:

@@ -219,12 +219,12 @@ std::tuple<Tensor, Tensor> combine_backward(const Tensor& dout_, const Tensor& y
     value(join({"dout has shape ", shape(dout), ", not [", num(p.T), ", ", num(H), "]"}));
   if (dout.scalar_type() != ys.scalar_type())
     type(join({"combine_backward: dout is ", c10::toString(dout.scalar_type()), ", ys ", c10::toString(ys.scalar_type())}));
-  on_device("combine_backward", {&ys, &dout, &w, &pos, &offsets});
+  on_device("combine_backward", {&ys, &dout, &w, &pos, &order, &offsets});
   const Tensor dys = make({p.n, H}, ys, ys.scalar_type()), dw = make({p.T, k}, ys, at::kFloat);
   run(ys, [&, &ys = ys, &w = w](pgemm_handle_t h) {
-    return pgemm_moe_combine_backward(h, ptr(dout), dout.stride(0), ptr(ys), ys.stride(0), ptr<float>(w), ptr<int32_t>(offsets),
-                                      ptr<int32_t>(pos), p.T, k, offsets.numel() - 1, H, dtype_of(ys, "ys"), ptr(dys),
-                                      ptr<float>(dw));
+    return pgemm_moe_combine_backward_plan(h, ptr(dout), dout.stride(0), ptr(ys), ys.stride(0), ptr<float>(w),
+                                           ptr<int32_t>(offsets), ptr<int32_t>(order), ptr<int32_t>(pos), p.T, k,
+                                           offsets.numel() - 1, H, dtype_of(ys, "ys"), ptr(dys), ptr<float>(dw));
   });
   return {dys, dw};
 }

@@ -100,7 +100,10 @@ hipError_t launch_back_k(pgemm_ctx* h, const moe::BackArgs& a, unsigned grid) {
 
 template <int DT>
 hipError_t launch_back(pgemm_ctx* h, const moe::BackArgs& a, int access) {
-  const unsigned grid = (unsigned)a.token_blocks + kClearBlocks;
+  // with the plan's order every sorted row is looked at: more workgroups for many rows, as far as a launch has room
+  const unsigned room = UINT32_MAX / moe::kThreads - (unsigned)a.token_blocks;
+  const unsigned looks = a.order ? (unsigned)a.n / 1024 : 0, clear = looks < kClearBlocks ? kClearBlocks : looks < 2048 ? looks : 2048;
+  const unsigned grid = (unsigned)a.token_blocks + (clear < room ? clear : room);
   const bool wide = lanes_of(a.H) == 256;
   if (access == moe::kStream) return launch_back_k<DT, moe::kStream, 256>(h, a, grid);
   if (access == moe::kAligned)
@@ -136,6 +139,44 @@ int sum_impl(pgemm_handle_t h, const void* rows, int64_t ld, const float* w, con
     return launch_status(h, bf16 ? launch_sum<kBF16, true>(h, a, access) : launch_sum<kF16, true>(h, a, access), "combine");
   return launch_status(h, bf16 ? launch_sum<kBF16, false>(h, a, access) : launch_sum<kF16, false>(h, a, access),
                        "dispatch backward");
+}
+
+int back_impl(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys, const float* w,
+              const int32_t* offsets, const int32_t* order, const int32_t* pos, int64_t T, int64_t k, int64_t E, int64_t H,
+              int dtype, void* dys, float* dw) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  int rc = check_rows(h, T, k, H, dtype);
+  if (rc == PGEMM_OK) rc = check_experts(h, E);
+  if (rc != PGEMM_OK) return rc;
+  if (T == 0) return PGEMM_OK;
+  if (!w || !offsets || !pos || !dw || (H > 0 && (!dout || !ys || !dys)))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  if (lddout < 0 || ldys < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "row strides %lld, %lld", (long long)lddout, (long long)ldys);
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  moe::BackArgs a;
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.lddout = lddout;
+  a.ys = static_cast<const uint16_t*>(ys);
+  a.ldys = ldys;
+  a.w = w;
+  a.pos = pos;
+  a.offsets = offsets;
+  a.order = order;
+  a.dys = static_cast<uint16_t*>(dys);
+  a.dw = dw;
+  a.T = (int)T;
+  a.k = (int)k;
+  a.E = (int)E;
+  a.H = (int)H;
+  a.n = (int)(T * k);
+  a.token_blocks = (int)token_blocks(T, H);
+  const bool al = H % 8 == 0 && lddout % 8 == 0 && ldys % 8 == 0 && aligned16(dout) && aligned16(ys) && aligned16(dys);
+  const int access = access_of(al, T * k, H);
+  return launch_status(h, dtype == PGEMM_BF16 ? launch_back<kBF16>(h, a, access) : launch_back<kF16>(h, a, access),
+                       "combine backward");
 }
 
 } // namespace
@@ -215,38 +256,14 @@ int pgemm_moe_combine(pgemm_handle_t h, const void* ys, int64_t ldys, const floa
 int pgemm_moe_combine_backward(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
                                const float* w, const int32_t* offsets, const int32_t* pos, int64_t T, int64_t k,
                                int64_t E, int64_t H, int dtype, void* dys, float* dw) {
-  if (!h) return PGEMM_ERR_INVALID_ARG;
-  h->last_error[0] = 0;
-  int rc = check_rows(h, T, k, H, dtype);
-  if (rc == PGEMM_OK) rc = check_experts(h, E);
-  if (rc != PGEMM_OK) return rc;
-  if (T == 0) return PGEMM_OK;
-  if (!w || !offsets || !pos || !dw || (H > 0 && (!dout || !ys || !dys)))
-    return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
-  if (lddout < 0 || ldys < 0)
-    return fail(h, PGEMM_ERR_INVALID_ARG, "row strides %lld, %lld", (long long)lddout, (long long)ldys);
-  DeviceScope dev(h->device);
-  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
-  moe::BackArgs a;
-  a.dout = static_cast<const uint16_t*>(dout);
-  a.lddout = lddout;
-  a.ys = static_cast<const uint16_t*>(ys);
-  a.ldys = ldys;
-  a.w = w;
-  a.pos = pos;
-  a.offsets = offsets;
-  a.dys = static_cast<uint16_t*>(dys);
-  a.dw = dw;
-  a.T = (int)T;
-  a.k = (int)k;
-  a.E = (int)E;
-  a.H = (int)H;
-  a.n = (int)(T * k);
-  a.token_blocks = (int)token_blocks(T, H);
-  const bool al = H % 8 == 0 && lddout % 8 == 0 && ldys % 8 == 0 && aligned16(dout) && aligned16(ys) && aligned16(dys);
-  const int access = access_of(al, T * k, H);
-  return launch_status(h, dtype == PGEMM_BF16 ? launch_back<kBF16>(h, a, access) : launch_back<kF16>(h, a, access),
-                       "combine backward");
+  return back_impl(h, dout, lddout, ys, ldys, w, offsets, nullptr, pos, T, k, E, H, dtype, dys, dw);
+}
+
+int pgemm_moe_combine_backward_plan(pgemm_handle_t h, const void* dout, int64_t lddout, const void* ys, int64_t ldys,
+                                    const float* w, const int32_t* offsets, const int32_t* order, const int32_t* pos,
+                                    int64_t T, int64_t k, int64_t E, int64_t H, int dtype, void* dys, float* dw) {
+  if (h && T > 0 && !order) return fail(h, PGEMM_ERR_INVALID_ARG, "order is NULL");
+  return back_impl(h, dout, lddout, ys, ldys, w, offsets, order, pos, T, k, E, H, dtype, dys, dw);
 }
 
 } // extern "C"

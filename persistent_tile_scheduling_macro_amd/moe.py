@@ -26,7 +26,8 @@ from . import _ops
 class RoutePlan:
     """Where the T*k slots of a batch went: what ``dispatch`` returns and the other steps read.
 
-    offsets int32 [E+1], order int32 [T*k], pos int32 [T*k] (see pgemm.h), and k, the slots of a token.
+    offsets int32 [E+1], order int32 [T*k], pos int32 [T*k] (see pgemm.h), and k, the slots of a token. A slot is taken
+    out afterwards by setting its pos to -1 (its row stays where it is, without a share and with a gradient of zeros).
     """
 
     __slots__ = ("offsets", "order", "pos", "k")
