@@ -487,6 +487,29 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a, int64_t lda, cons
  * A pure function. */
 int pgemm_grouped_weight_grad_workspace(int64_t R, int64_t E, int64_t I, int64_t J, int64_t* bytes);
 
+/* Body of a grouped product. ANY: 128 x 128 tiles, operands of any alignment;
+ * PINGPONG: 256 x 256 tiles, persistent; FEW16, FEW16_WIDE, FEW32_WIDE: 16 or 32
+ * rows at once (WIDE: two column blocks of N x K matrices); FEW_GRAD: the weight
+ * gradient of few rows. */
+typedef enum {
+  PGEMM_GROUPED_ANY = 0,
+  PGEMM_GROUPED_PINGPONG = 1,
+  PGEMM_GROUPED_FEW16 = 2,
+  PGEMM_GROUPED_FEW16_WIDE = 3,
+  PGEMM_GROUPED_FEW32_WIDE = 4,
+  PGEMM_GROUPED_FEW_GRAD = 5
+} pgemm_grouped_body_t;
+
+/* Report the body that pgemm_grouped_run would launch. `wide` tells whether
+ * every operand's rows lie at 16-byte addresses (which PINGPONG needs, next to
+ * K and N of a multiple of 8). A pure function. PGEMM_ERR_INVALID_ARG for a
+ * NULL pointer, a size below 1 or an unknown layout. */
+int pgemm_grouped_query(int64_t R, int64_t E, int64_t K, int64_t N, int layout, int wide, int* body);
+
+/* The same for pgemm_grouped_weight_grad, and the pieces an expert's rows are
+ * cut into. */
+int pgemm_grouped_weight_grad_query(int64_t R, int64_t E, int64_t I, int64_t J, int wide, int* body, int* pieces);
+
 /* ---- few rows times 4-bit weights -------------------------------------- */
 
 /* Format of the 4-bit codes. INT4: whole numbers 0..15 less a zero point;
@@ -518,6 +541,12 @@ typedef enum { PGEMM_W4_INT4 = 0, PGEMM_W4_E2M1 = 1 } pgemm_w4_format_t;
 int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, const void* scales, const void* zeros,
                  const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K, int64_t E, int group, int fmt,
                  int dtype);
+
+/* Report the form that pgemm_w4_run would launch on a device of `cus` CUs:
+ * rows of x at once (4, 16 or 32) and blocks of 16 columns a wave takes (1 or
+ * 2). `experts`: nonzero with offsets. A pure function. PGEMM_ERR_INVALID_ARG
+ * for a NULL pointer or a size below 1. */
+int pgemm_w4_query(int64_t M, int64_t N, int64_t E, int experts, int cus, int* rows, int* blocks);
 
 /* Benchmark aid, not part of the GEMM: make about `n_cus` CUs of device
  * `device` unavailable for about `microseconds`, asynchronously on the HIP

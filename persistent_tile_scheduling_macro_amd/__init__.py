@@ -42,6 +42,13 @@ PGEMM_B_NK = 1
 PGEMM_IDS_I32 = 0
 PGEMM_IDS_I64 = 1
 
+PGEMM_GROUPED_ANY = 0
+PGEMM_GROUPED_PINGPONG = 1
+PGEMM_GROUPED_FEW16 = 2
+PGEMM_GROUPED_FEW16_WIDE = 3
+PGEMM_GROUPED_FEW32_WIDE = 4
+PGEMM_GROUPED_FEW_GRAD = 5
+
 PGEMM_W4_INT4 = 0
 PGEMM_W4_E2M1 = 1
 
@@ -122,6 +129,9 @@ _grouped_weight_grad = _sig("pgemm_grouped_weight_grad", _int, _vp, _vp, _i64, _
 _grouped_weight_grad_workspace = _sig("pgemm_grouped_weight_grad_workspace", _int, _i64, _i64, _i64, _i64,
                                       ctypes.POINTER(_i64))
 _w4_run = _sig("pgemm_w4_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int)
+_grouped_query = _sig("pgemm_grouped_query", _int, _i64, _i64, _i64, _i64, _int, _int, _ip)
+_grouped_weight_grad_query = _sig("pgemm_grouped_weight_grad_query", _int, _i64, _i64, _i64, _i64, _int, _ip, _ip)
+_w4_query = _sig("pgemm_w4_query", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
 
@@ -358,6 +368,27 @@ def pgemm_w4_run(h, x, ldx: int, q, scales, zeros, offsets, y, M: int, N: int, K
     """Enqueue y = x times 4-bit weights with group scales (pointers or tensors; zeros and offsets may be None)."""
     _check(_w4_run(h, _ptr(x), ldx, _ptr(q), _ptr(scales), _ptr(zeros) or None, _ptr(offsets) or None, _ptr(y), M, N, K,
                    E, group, fmt, dtype), h)
+
+
+def pgemm_grouped_query(R: int, E: int, K: int, N: int, layout: int, wide: bool = True) -> int:
+    """The PGEMM_GROUPED_* body that pgemm_grouped_run would launch."""
+    body = _int()
+    _check(_grouped_query(R, E, K, N, layout, int(wide), ctypes.byref(body)))
+    return body.value
+
+
+def pgemm_grouped_weight_grad_query(R: int, E: int, I: int, J: int, wide: bool = True) -> tuple:
+    """(PGEMM_GROUPED_* body, pieces an expert's rows are cut into) of pgemm_grouped_weight_grad."""
+    body, pieces = _int(), _int()
+    _check(_grouped_weight_grad_query(R, E, I, J, int(wide), ctypes.byref(body), ctypes.byref(pieces)))
+    return body.value, pieces.value
+
+
+def pgemm_w4_query(M: int, N: int, E: int = 1, experts: bool = False, cus: int = 256) -> tuple:
+    """(rows at once, blocks of 16 columns a wave takes) of pgemm_w4_run."""
+    rows, blocks = _int(), _int()
+    _check(_w4_query(M, N, E, int(experts), cus, ctypes.byref(rows), ctypes.byref(blocks)))
+    return rows.value, blocks.value
 
 
 def matmul(A, B, C=None, *, sched: str | int = "static", grid_multiple: int = 0, handle=None):

@@ -22,6 +22,11 @@ int check(pgemm_ctx* h, int64_t R, int64_t E, int64_t K, int64_t N, int64_t lda,
 
 bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
 
+static_assert(grouped::kAnyAlignment == PGEMM_GROUPED_ANY && grouped::kPingPong == PGEMM_GROUPED_PINGPONG &&
+                  grouped::kFew16 == PGEMM_GROUPED_FEW16 && grouped::kFew16Wide == PGEMM_GROUPED_FEW16_WIDE &&
+                  grouped::kFew32Wide == PGEMM_GROUPED_FEW32_WIDE && grouped::kFewGrad == PGEMM_GROUPED_FEW_GRAD,
+              "the query's numbers are the bodies'");
+
 // Tile of a body: rows, columns, threads.
 struct Shape { int bm, bn, threads; };
 Shape shape_of(int body, bool nk) {
@@ -118,6 +123,13 @@ GradPlan plan_grad(int64_t R, int64_t E, int64_t I, int64_t J) {
   return best;
 }
 
+// Plan of the gradient form for operands that can, or cannot, be copied directly.
+GradPlan plan_grad_for(int64_t R, int64_t E, int64_t I, int64_t J, bool direct) {
+  GradPlan p = plan_grad(R, E, I, J);
+  if (!direct && p.body != grouped::kFewGrad) p.body = grouped::kAnyAlignment; // the workspace is the same either way
+  return p;
+}
+
 // tile_rows(bm): upper bound of the tile rows of height bm over all experts.
 template <class F>
 int launch(pgemm_ctx* h, grouped::Args a, int body, F tile_rows, int dtype, bool grad, bool nk) {
@@ -179,6 +191,27 @@ int pgemm_grouped_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* 
   return launch(h, a, pick_rows_body(a, direct, nk), [&](int bm) { return R / bm + E + 1; }, dtype, false, nk);
 }
 
+int pgemm_grouped_query(int64_t R, int64_t E, int64_t K, int64_t N, int layout, int wide, int* body) {
+  if (!body || R < 1 || E < 1 || K < 1 || N < 1 || (layout != PGEMM_B_KN && layout != PGEMM_B_NK)) return PGEMM_ERR_INVALID_ARG;
+  if (R > kMaxSize || K > kMaxSize || N > kMaxSize || E > moe::kMaxExperts) return PGEMM_ERR_UNSUPPORTED;
+  grouped::Args a = {};
+  a.R = (int)R;
+  a.E = (int)E;
+  a.K = (int)K;
+  a.N = (int)N;
+  *body = pick_rows_body(a, wide && K % 8 == 0 && N % 8 == 0, layout == PGEMM_B_NK);
+  return PGEMM_OK;
+}
+
+int pgemm_grouped_weight_grad_query(int64_t R, int64_t E, int64_t I, int64_t J, int wide, int* body, int* pieces) {
+  if (!body || !pieces || R < 1 || E < 1 || I < 1 || J < 1) return PGEMM_ERR_INVALID_ARG;
+  if (R > kMaxSize || I > kMaxSize || J > kMaxSize || E > moe::kMaxExperts) return PGEMM_ERR_UNSUPPORTED;
+  const GradPlan p = plan_grad_for(R, E, I, J, wide && I % 8 == 0 && J % 8 == 0);
+  *body = p.body;
+  *pieces = (int)p.pieces;
+  return PGEMM_OK;
+}
+
 int pgemm_grouped_weight_grad_workspace(int64_t R, int64_t E, int64_t I, int64_t J, int64_t* bytes) {
   if (!bytes || R < 0 || E < 1 || I < 0 || J < 0) return PGEMM_ERR_INVALID_ARG;
   *bytes = 0;
@@ -214,13 +247,12 @@ int pgemm_grouped_weight_grad(pgemm_handle_t h, const void* a_rows, int64_t lda,
   a.E = (int)E;
   a.M = (int)I;
   a.N = (int)J;
-  const GradPlan plan = plan_grad(R, E, I, J);
-  a.split = (int)plan.pieces;
   a.part = static_cast<float*>(work);
   const bool direct = I % 8 == 0 && J % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && lda <= kMaxDirectStride &&
                       ldb <= kMaxDirectStride && aligned16(a_rows) && aligned16(b_rows) && aligned16(c);
-  const int body = direct || plan.body == grouped::kFewGrad ? plan.body : grouped::kAnyAlignment;
-  return launch(h, a, body, [&](int bm) { return E * a.split * ((I + bm - 1) / bm); }, dtype, true, false);
+  const GradPlan plan = plan_grad_for(R, E, I, J, direct);
+  a.split = (int)plan.pieces;
+  return launch(h, a, plan.body, [&](int bm) { return E * a.split * ((I + bm - 1) / bm); }, dtype, true, false);
 }
 
 } // extern "C"

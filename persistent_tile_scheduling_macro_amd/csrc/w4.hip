@@ -4,6 +4,30 @@
 
 using namespace pgemm;
 
+namespace {
+
+struct Form { int rows, blocks; };
+Form pick_form(int64_t M, int64_t N, int64_t E, bool offsets, int cus) {
+  // Rows a workgroup takes at once. An expert's rows are known only on the device: twice the mean
+  // covers most experts in one pass, and a longer one loops.
+  const int64_t mean = offsets ? (2 * M + E - 1) / E : M;
+  // Columns a wave takes: two blocks share the reads of x, one where two would leave CUs idle.
+  const int64_t experts = offsets ? (E < M ? E : M) : 1;
+  return {mean <= 4 ? 4 : mean <= 16 ? 16 : 32, experts * ((N + 31) / 32) >= 2 * cus ? 2 : 1};
+}
+
+} // namespace
+
+extern "C" int pgemm_w4_query(int64_t M, int64_t N, int64_t E, int experts, int cus, int* rows, int* blocks) {
+  if (!rows || !blocks || M < 1 || N < 1 || E < 1 || cus < 1) return PGEMM_ERR_INVALID_ARG;
+  constexpr int64_t lim = (int64_t)1 << 30;
+  if (M > lim || N > lim || E > 65534) return PGEMM_ERR_UNSUPPORTED;
+  const Form f = pick_form(M, N, E, experts != 0, cus);
+  *rows = f.rows;
+  *blocks = f.blocks;
+  return PGEMM_OK;
+}
+
 extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, const void* scales,
                             const void* zeros, const int32_t* offsets, void* y, int64_t M, int64_t N, int64_t K,
                             int64_t E, int group, int fmt, int dtype) {
@@ -43,13 +67,7 @@ extern "C" int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const 
   a.E = (int)E;
   a.row_bytes = (int)((K + 1) / 2);
   a.groups = (int)((K + group - 1) / group);
-  // Rows a workgroup takes at once. An expert's rows are known only on the device: twice the mean
-  // covers most experts in one pass, and a longer one loops.
-  const int64_t mean = offsets ? (2 * M + E - 1) / E : M;
-  const int rows = mean <= 4 ? 4 : mean <= 16 ? 16 : 32;
-  // Columns a wave takes: two blocks share the reads of x, one where two would leave CUs idle.
-  const int64_t experts = offsets ? (E < M ? E : M) : 1;
-  const int cb = experts * ((N + 31) / 32) >= 2 * h->cus ? 2 : 1;
+  const auto [rows, cb] = pick_form(M, N, E, offsets != nullptr, h->cus);
   const int64_t row_groups = offsets ? E + 1 : (M + rows - 1) / rows;
   const int64_t cols = (N + 16 * cb - 1) / (16 * cb);
   if (cols * w4::waves_of(rows) * 64 > UINT32_MAX) // threads of a launch
