@@ -1,5 +1,6 @@
 """Build libpgemm.so (the HIP kernels and the C-ABI host code) for gfx950, and
-_ops.so, the torch binding of the operators (host code, linked to it).
+_ops.so, the torch binding of the operators (host code, linked to it; left out
+where torch for ROCm is not installed: the C library does not need it).
 
 Each translation unit is compiled in parallel with hipcc, then linked into
 one shared library next to this file. Run as ``python -m
@@ -76,9 +77,16 @@ def _compile(src: str):
     return obj, parse_resource_remarks(r.stderr)
 
 
-def _build_ops(tmp: str) -> None:
+def _torch_for_rocm():
+    """torch's folder, or None if there is no torch here, or one without ROCm's libraries or its headers."""
+    spec = importlib.util.find_spec("torch")
+    root = os.path.dirname(spec.origin) if spec is not None and spec.origin else ""
+    needed = ("lib/libc10_hip.so", "lib/libtorch_hip.so", "include/ATen/core/Tensor.h", "include/c10/hip/HIPStream.h")
+    return root if root and all(os.path.exists(os.path.join(root, f)) for f in needed) else None
+
+
+def _build_ops(torch: str, tmp: str) -> None:
     """Compile the binding against torch's headers and the library just linked."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM=1", "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
@@ -111,7 +119,14 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_ops(OPS + ".tmp")
+    torch = _torch_for_rocm()
+    if torch is None:
+        if os.path.exists(OPS):
+            os.remove(OPS)  # it belongs to another build of the library
+        print(f"built {LIB}; torch for ROCm and its headers were not found, so the torch binding {OPS} was not built "
+              "(the modules moe and w4 need it)")
+        return LIB
+    _build_ops(torch, OPS + ".tmp")
     os.replace(OPS + ".tmp", OPS)
     if verbose:
         print(f"built {LIB} and {OPS}")
