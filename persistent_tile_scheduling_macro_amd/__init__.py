@@ -66,15 +66,17 @@ if not os.path.exists(LIB_PATH):
                       "`python -m persistent_tile_scheduling_macro_amd.build` (hipcc, gfx950)")
 
 
-
 def _load_hip_runtime() -> None:
     """Load torch's own HIP runtime before the library asks for one, whichever of the two is imported first: a process
-    that holds both it and the system's passes streams of one to the other."""
-    torch = importlib.util.find_spec("torch")
-    if torch is not None and torch.origin:
-        path = os.path.join(os.path.dirname(torch.origin), "lib", "libamdhip64.so")
-        if os.path.exists(path):
-            ctypes.CDLL(path)
+    that holds both it and the system's passes streams of one to the other. Without a torch that has one, the system's."""
+    try:
+        torch = importlib.util.find_spec("torch")
+        if torch is not None and torch.origin:
+            path = os.path.join(os.path.dirname(torch.origin), "lib", "libamdhip64.so")
+            if os.path.exists(path):
+                ctypes.CDLL(path)
+    except (ValueError, OSError):  # a module without a spec in torch's place, a runtime that does not load
+        pass
 
 
 _load_hip_runtime()
