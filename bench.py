@@ -145,16 +145,17 @@ PROFILES = os.path.join(ROOT, "profiles")
 
 
 def source_digest() -> str:
-    """sha256 over the GEMM's sources' code (comments and blank space removed);
-    HBM counters are only reported for the code they came from. The routed
-    operators and the 4-bit product have sources of their own, which the timed
-    workloads do not run."""
+    """sha256 over the code (comments and blank space removed) that decides what the
+    GEMM's launches move: its kernels and the launch planner. HBM counters are only
+    reported for the code they came from. Left out are the host's declarations of the
+    handle and of the launch call, and the sources of the routed operators and the
+    4-bit product, which the timed workloads do not run."""
     import hashlib
     import re
 
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".h", ".hip")) and not name.startswith(("moe", "grouped", "w4")):
+        if name.endswith((".h", ".hip")) and not name.startswith(("moe", "grouped", "w4", "context.h", "launch.h")):
             with open(os.path.join(CSRC, name), encoding="utf-8") as f:
                 text = f.read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
