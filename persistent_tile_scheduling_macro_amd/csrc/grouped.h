@@ -3,8 +3,9 @@
 //   rows form:      c[r][n] = sum_k a[r][k] * b[e(r)][k][n]     (the forward product, and the
 //                   gradient of its rows with the other layout of b)
 //   gradient form:  c[e][i][j] = sum over e's rows r of a[r][i] * b[r][j]
-// Sums are fp32, in the order of k, rounded once; each output tile is one
-// workgroup's, so a result does not depend on which workgroup runs when.
+// Sums are fp32, in an order that the sizes fix, rounded once: along k, in the few-row bodies eight waves' shares of it
+// and in a split gradient the pieces, joined in order. Each output tile (or piece) is one workgroup's, so a result does
+// not depend on which workgroup runs when.
 //
 // An operand is "k-contiguous" (kc: its rows run along the sum) or
 // "outer-contiguous" (oc: its rows run along an output axis). LDS tiles and

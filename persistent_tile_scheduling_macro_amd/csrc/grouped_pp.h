@@ -12,15 +12,17 @@
 // * A tile without a sum (an expert or a gap without rows to sum over) runs
 //   two steps whose copies are all masked and read zeros.
 //
-// 32768 rows over 32 experts, 4096 x 2048 bf16: forward and rows' gradient 503
-// to 510 us (1080 TFLOP/s, MFMAs busy 0.55 to 0.59 at the clock that power
-// allows; torch's product of 8192^3 runs at 1222 on the same card), weight
-// gradient 640 us (860): its tiles sum 16 steps only and store 128 KiB each,
-// 537 MB in all. Measured and not kept: tile heights that divide an expert's
-// rows evenly with the MFMAs of empty row blocks left out (the jumps between
-// the MFMAs cost 7% of full tiles, and partial tiles, whose copies and reads
-// bound them, gained nothing); nontemporal stores of c (6% slower: a store
-// covers half lines); a tile's stores after the next tile's copies (spills).
+// 32768 rows over 32 experts, 4096 x 2048 bf16, product and both gradients in turn: with N x K matrices 490 us (1120
+// TFLOP/s), with K x N 520 us (1060), weight gradient 583 us (940), either operand as its rows; its tiles sum 16 steps
+// only and store 128 KiB each, 537 MB in all. (Under the profiler's trace 535, 571 and 643 us, MFMAs busy 0.59, 0.55 and
+// 0.46 at the clock that power allows; torch's product of 8192^3 runs at 1222 TFLOP/s on the same card.)
+// With fewer tiles than workgroups, in a launch's last part round, and with a grid of no multiple of 8, tiles are
+// taken in plain order: neighbours, which share rows and a matrix, go to eight L2s. 8200 rows over seven experts, rows of
+// 2056 fp16 to 1000: 144 tiles read 202 MB of 58 and take 57 us, where the choosing rule's estimate is 42.
+// Measured and not kept: tile heights that divide an expert's rows evenly with the MFMAs of empty row blocks left out
+// (the jumps between the MFMAs cost 7% of full tiles, and partial tiles, whose copies and reads bound them, gained
+// nothing); nontemporal stores of c (6% slower: a store covers half lines); a tile's stores after the next tile's
+// copies (spills).
 #pragma once
 
 #include "gemm_pingpong.h"
