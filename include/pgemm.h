@@ -548,6 +548,83 @@ int pgemm_w4_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* q, co
  * for a NULL pointer or a size below 1. */
 int pgemm_w4_query(int64_t M, int64_t N, int64_t E, int experts, int cus, int* rows, int* blocks);
 
+/* ---- the linear layer -------------------------------------------------- */
+/*
+ * z = x W + bias, y = act(z) + residual; gated: W and bias have 2N columns,
+ * the gate's first, and y = act(z[:, :N]) * z[:, N:] + residual. C below is the
+ * number of W's columns, N or 2N.
+ *   x: M rows of K; W: [K, C] for PGEMM_B_KN, [C, K] for PGEMM_B_NK, rows ldw
+ *   apart; bias: [C]; residual: M rows of N; y: [M, N]; z: [M, C], contiguous.
+ * dtype is PGEMM_F16 or PGEMM_BF16, of every matrix and vector. ld* is the
+ * distance of two rows in elements (0 repeats one row). Sums, activations and
+ * column sums are fp32; y, z and each gradient are rounded once (dz, the
+ * gradient of z, too: it is an operand of the two products), the same on every
+ * run. Sizes may be odd and addresses any that elements have; rows of a multiple
+ * of 8 elements at 16-byte addresses are the fastest (others are moved to the
+ * workspace first where M exceeds 32). `work` is device memory at a multiple of
+ * 16, of at least the bytes that the workspace functions report, free again
+ * once the call's work is done; nothing is allocated. Empty sums give the
+ * epilogue of zero.
+ * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size or
+ * stride, an unknown layout, activation or type, or too small a workspace;
+ * PGEMM_ERR_UNSUPPORTED for K or C above 2^21 or more tiles than one launch
+ * takes (2^21 of 64 x 128, of any two of M, C, K). */
+
+/* Activations. GELU: x Phi(x); GELU_TANH: its form with tanh; SILU: x / (1 + exp(-x)). */
+typedef enum {
+  PGEMM_ACT_NONE = 0,
+  PGEMM_ACT_RELU = 1,
+  PGEMM_ACT_GELU = 2,
+  PGEMM_ACT_GELU_TANH = 3,
+  PGEMM_ACT_SILU = 4
+} pgemm_act_t;
+
+/* Enqueue y, and z unless it is NULL. bias and residual may be NULL. */
+int pgemm_dense_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                    const void* residual, int64_t ldr, void* y, void* z, int64_t M, int64_t N, int64_t K, int layout,
+                    int act, int gated, int dtype, void* work, int64_t work_bytes);
+
+/* Bytes of scratch that pgemm_dense_run needs. `wide` tells whether the rows of
+ * x and W lie at 16-byte addresses, at most 2^21 elements apart. A pure function. */
+int pgemm_dense_workspace(int64_t M, int64_t N, int64_t K, int layout, int gated, int wide, int64_t* bytes);
+
+/* Enqueue the gradients from that of y: dx [M, K], dw like W (contiguous), db
+ * [C], each unless it is NULL. z as pgemm_dense_run left it (NULL for
+ * PGEMM_ACT_NONE without a gate). The residual's gradient is dy itself. */
+int pgemm_dense_backward(pgemm_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                         int64_t ldw, const void* z, void* dx, void* dw, void* db, int64_t M, int64_t N, int64_t K,
+                         int layout, int act, int gated, int dtype, void* work, int64_t work_bytes);
+
+/* Gradients asked for, added up. */
+typedef enum { PGEMM_DENSE_DX = 1, PGEMM_DENSE_DW = 2, PGEMM_DENSE_DB = 4 } pgemm_dense_needs_t;
+
+/* Bytes of scratch that pgemm_dense_backward needs for these gradients; `wide`
+ * as above, for dy, x and W. A pure function. */
+int pgemm_dense_backward_workspace(int64_t M, int64_t N, int64_t K, int layout, int act, int gated, int needs, int wide,
+                                   int64_t* bytes);
+
+/* Body of a product of the linear layer. FEW8, FEW16, FEW32: so many rows at
+ * once; TILE64, TILE128: tiles of 64 or 128 x 128; TILE128_PAIR: the same, two
+ * to a CU; PINGPONG: 256 x 256 tiles, persistent. */
+typedef enum {
+  PGEMM_DENSE_FEW8 = 0,
+  PGEMM_DENSE_FEW16 = 1,
+  PGEMM_DENSE_FEW32 = 2,
+  PGEMM_DENSE_TILE64 = 3,
+  PGEMM_DENSE_TILE128 = 4,
+  PGEMM_DENSE_TILE128_PAIR = 5,
+  PGEMM_DENSE_PINGPONG = 6
+} pgemm_dense_body_t;
+
+/* Report the body that pgemm_dense_run would launch and the pieces it cuts the
+ * sum into. (The gradient of x is the product of M, K, C with the other layout
+ * and no gate.) Pure functions. PGEMM_ERR_INVALID_ARG for a NULL pointer or a
+ * size below 1. */
+int pgemm_dense_query(int64_t M, int64_t N, int64_t K, int layout, int gated, int* body, int* pieces);
+
+/* The same for the gradient of W: [I, J] = a^T b over R rows. */
+int pgemm_dense_weight_grad_query(int64_t R, int64_t I, int64_t J, int* body, int* pieces);
+
 /* Benchmark aid, not part of the GEMM: make about `n_cus` CUs of device
  * `device` unavailable for about `microseconds`, asynchronously on the HIP
  * stream `hip_stream` (NULL = null stream). It launches n_cus workgroups

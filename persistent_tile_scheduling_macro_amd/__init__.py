@@ -52,6 +52,24 @@ PGEMM_GROUPED_FEW_GRAD = 5
 PGEMM_W4_INT4 = 0
 PGEMM_W4_E2M1 = 1
 
+PGEMM_ACT_NONE = 0
+PGEMM_ACT_RELU = 1
+PGEMM_ACT_GELU = 2
+PGEMM_ACT_GELU_TANH = 3
+PGEMM_ACT_SILU = 4
+
+PGEMM_DENSE_DX = 1
+PGEMM_DENSE_DW = 2
+PGEMM_DENSE_DB = 4
+
+PGEMM_DENSE_FEW8 = 0
+PGEMM_DENSE_FEW16 = 1
+PGEMM_DENSE_FEW32 = 2
+PGEMM_DENSE_TILE64 = 3
+PGEMM_DENSE_TILE128 = 4
+PGEMM_DENSE_TILE128_PAIR = 5
+PGEMM_DENSE_PINGPONG = 6
+
 PGEMM_MAINLOOP_AUTO = 0
 PGEMM_MAINLOOP_LOCKSTEP = 1
 PGEMM_MAINLOOP_PINGPONG = 2
@@ -134,6 +152,15 @@ _w4_run = _sig("pgemm_w4_run", _int, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i
 _grouped_query = _sig("pgemm_grouped_query", _int, _i64, _i64, _i64, _i64, _int, _int, _ip)
 _grouped_weight_grad_query = _sig("pgemm_grouped_weight_grad_query", _int, _i64, _i64, _i64, _i64, _int, _ip, _ip)
 _w4_query = _sig("pgemm_w4_query", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
+_dense_run = _sig("pgemm_dense_run", _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _int,
+                  _int, _int, _vp, _i64)
+_dense_workspace = _sig("pgemm_dense_workspace", _int, _i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(_i64))
+_dense_backward = _sig("pgemm_dense_backward", _int, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                       _int, _int, _int, _int, _vp, _i64)
+_dense_backward_workspace = _sig("pgemm_dense_backward_workspace", _int, _i64, _i64, _i64, _int, _int, _int, _int, _int,
+                                 ctypes.POINTER(_i64))
+_dense_query = _sig("pgemm_dense_query", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
+_dense_weight_grad_query = _sig("pgemm_dense_weight_grad_query", _int, _i64, _i64, _i64, _ip, _ip)
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
 
@@ -304,6 +331,49 @@ def pgemm_read_work_counter(h) -> int:
     v = ctypes.c_int32()
     _check(_read_work_counter(h, ctypes.byref(v)), h)
     return v.value
+
+
+def pgemm_dense_run(h, x, ldx: int, w, ldw: int, bias, residual, ldr: int, y, z, M: int, N: int, K: int, layout: int, act: int,
+                    gated: int, dtype: int, work=None, work_bytes: int = 0) -> None:
+    """Enqueue y = act(x W + bias) + residual, and z, its pre-activations, unless None."""
+    _check(_dense_run(h, _ptr(x), ldx, _ptr(w), ldw, _ptr(bias) or None, _ptr(residual) or None, ldr, _ptr(y), _ptr(z) or None,
+                      M, N, K, layout, act, gated, dtype, _ptr(work) or None, work_bytes), h)
+
+
+def pgemm_dense_workspace(M: int, N: int, K: int, layout: int, gated: int = 0, wide: bool = True) -> int:
+    """Bytes of device scratch that pgemm_dense_run needs."""
+    v = _i64()
+    _check(_dense_workspace(M, N, K, layout, gated, int(wide), ctypes.byref(v)))
+    return v.value
+
+
+def pgemm_dense_backward(h, dy, lddy: int, x, ldx: int, w, ldw: int, z, dx, dw, db, M: int, N: int, K: int, layout: int, act: int,
+                         gated: int, dtype: int, work=None, work_bytes: int = 0) -> None:
+    """Enqueue the gradients dx, dw and db, each unless None."""
+    _check(_dense_backward(h, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), ldw, _ptr(z) or None, _ptr(dx) or None, _ptr(dw) or None,
+                           _ptr(db) or None, M, N, K, layout, act, gated, dtype, _ptr(work) or None, work_bytes), h)
+
+
+def pgemm_dense_backward_workspace(M: int, N: int, K: int, layout: int, act: int, gated: int = 0, needs: int = 7,
+                                   wide: bool = True) -> int:
+    """Bytes of device scratch that pgemm_dense_backward needs for the gradients in `needs` (PGEMM_DENSE_D*, added up)."""
+    v = _i64()
+    _check(_dense_backward_workspace(M, N, K, layout, act, gated, needs, int(wide), ctypes.byref(v)))
+    return v.value
+
+
+def pgemm_dense_query(M: int, N: int, K: int, layout: int, gated: int = 0) -> tuple:
+    """(PGEMM_DENSE_* body, pieces of the sum) of pgemm_dense_run."""
+    body, pieces = ctypes.c_int(), ctypes.c_int()
+    _check(_dense_query(M, N, K, layout, gated, ctypes.byref(body), ctypes.byref(pieces)))
+    return body.value, pieces.value
+
+
+def pgemm_dense_weight_grad_query(R: int, I: int, J: int) -> tuple:
+    """(PGEMM_DENSE_* body, pieces of the sum) of the linear layer's weight gradient, [I, J] over R rows."""
+    body, pieces = ctypes.c_int(), ctypes.c_int()
+    _check(_dense_weight_grad_query(R, I, J, ctypes.byref(body), ctypes.byref(pieces)))
+    return body.value, pieces.value
 
 
 def pgemm_hold_cus(stream, device: int, n_cus: int, microseconds: int) -> None:

@@ -1,4 +1,4 @@
-// torch binding of the routed operators and the 4-bit product (module _ops).
+// torch binding of the operators (module _ops): the routed ones, the 4-bit product, the linear layer.
 //
 // Checks shapes and types, makes the outputs and passes pointers to the C ABI
 // on torch's current stream: what a call of a few microseconds on the GPU can
@@ -331,6 +331,103 @@ Tensor w4(const Tensor& x_, const Tensor& q_, const Tensor& scales_, const c10::
   return y;
 }
 
+// ------------------------------------------------------------ the linear layer
+// Whether a matrix' rows can be copied in 16-byte chunks (one whose rows are further apart than a tile's offsets reach is moved).
+bool wide(const Tensor& t) {
+  return (uintptr_t)t.data_ptr() % 16 == 0 && t.stride(0) % 8 == 0 && t.stride(0) <= (int64_t)1 << 21;
+}
+using Maybe = c10::optional<Tensor>;
+
+struct Dense {
+  Tensor x, w;
+  int64_t M, N, K, C;
+};
+Dense check_dense(const char* name, const Tensor& x_, const Tensor& w_, bool nk, bool gated) {
+  const Tensor x = rows_of(x_, "x"), w = rows_of(w_, "w");
+  if (w.scalar_type() != x.scalar_type())
+    type(join({name, ": w is ", c10::toString(w.scalar_type()), ", x ", c10::toString(x.scalar_type())}));
+  const int64_t K = x.size(1), C = w.size(nk ? 0 : 1);
+  if (w.size(nk ? 1 : 0) != K)
+    value(join({name, ": w has shape ", shape(w), " for rows of ", num(K), " and layout ", nk ? "'nk'" : "'kn'"}));
+  if (gated && C % 2) value(join({name, ": w has ", num(C), " columns, which no gate halves"}));
+  on_device(name, {&x, &w});
+  return {x, w, x.size(0), gated ? C / 2 : C, K, C};
+}
+
+// A vector or matrix of x's type and the given shape.
+void same_kind(const char* name, const char* what, const Tensor& t, const Tensor& x, at::IntArrayRef sizes) {
+  if (t.scalar_type() != x.scalar_type())
+    type(join({name, ": ", what, " is ", c10::toString(t.scalar_type()), ", x ", c10::toString(x.scalar_type())}));
+  no_tangent(t, what);
+  if (t.sizes() != sizes) {
+    std::ostringstream s;
+    s << sizes;
+    value(join({name, ": ", what, " has shape ", shape(t), ", not ", s.str()}));
+  }
+  on_device(name, {&x, &t});
+}
+
+std::tuple<Tensor, Maybe> dense(const Tensor& x_, const Tensor& w_, const Maybe& bias_, const Maybe& residual_, int act, bool gated,
+                                bool nk, bool keep_z) {
+  const Dense d = check_dense("dense.matmul", x_, w_, nk, gated);
+  Tensor bias, residual;
+  if (bias_) {
+    same_kind("dense.matmul", "bias", *bias_, d.x, {d.C});
+    bias = bias_->contiguous();
+  }
+  if (residual_) {
+    same_kind("dense.matmul", "residual", *residual_, d.x, {d.M, d.N});
+    residual = rows_of(*residual_, "residual");
+  }
+  int64_t bytes = 0;
+  const int rc = pgemm_dense_workspace(d.M, d.N, d.K, nk ? PGEMM_B_NK : PGEMM_B_KN, gated, wide(d.x) && wide(d.w), &bytes);
+  if (rc != PGEMM_OK) raise(rc, "linear layer of " + num(d.M) + " rows, " + num(d.K) + " to " + num(d.C));
+  const Tensor y = make({d.M, d.N}, d.x, d.x.scalar_type());
+  Maybe z;
+  if (keep_z && (gated || act != PGEMM_ACT_NONE)) z = make({d.M, d.C}, d.x, d.x.scalar_type());
+  Tensor work;
+  if (bytes) work = make({bytes}, d.x, at::kByte);
+  run(d.x, [&](pgemm_handle_t h) {
+    return pgemm_dense_run(h, ptr(d.x), d.x.stride(0), ptr(d.w), d.w.stride(0), bias_ ? ptr(bias) : nullptr,
+                           residual_ ? ptr(residual) : nullptr, residual_ ? residual.stride(0) : 0, ptr(y), z ? ptr(*z) : nullptr,
+                           d.M, d.N, d.K, nk ? PGEMM_B_NK : PGEMM_B_KN, act, gated, dtype_of(d.x, "x"), bytes ? ptr(work) : nullptr,
+                           bytes);
+  });
+  return {y, z};
+}
+
+std::tuple<Maybe, Maybe, Maybe> dense_backward(const Tensor& dy_, const Tensor& x_, const Tensor& w_, const Maybe& z_, int act,
+                                               bool gated, bool nk, bool need_dx, bool need_dw, bool need_db) {
+  const Tensor dy = rows_of(dy_, "dy");
+  const Dense d = check_dense("dense.matmul_backward", x_, w_, nk, gated);
+  same_kind("dense.matmul_backward", "dy", dy, d.x, {d.M, d.N});
+  const bool slope = gated || act != PGEMM_ACT_NONE;
+  Tensor z;
+  if (slope) {
+    if (!z_) value("dense.matmul_backward: z, the pre-activations, are needed for this activation");
+    same_kind("dense.matmul_backward", "z", *z_, d.x, {d.M, d.C});
+    z = z_->contiguous();
+  }
+  Maybe dx, dw, db;
+  if (need_dx) dx = make({d.M, d.K}, d.x, d.x.scalar_type());
+  if (need_dw) dw = make(d.w.sizes(), d.x, d.x.scalar_type());
+  if (need_db) db = make({d.C}, d.x, d.x.scalar_type());
+  if (!need_dx && !need_dw && !need_db) return {dx, dw, db};
+  const int needs = need_dx * PGEMM_DENSE_DX + need_dw * PGEMM_DENSE_DW + need_db * PGEMM_DENSE_DB;
+  int64_t bytes = 0;
+  const int rc = pgemm_dense_backward_workspace(d.M, d.N, d.K, nk ? PGEMM_B_NK : PGEMM_B_KN, act, gated, needs,
+                                                wide(dy) && wide(d.x) && wide(d.w), &bytes);
+  if (rc != PGEMM_OK) raise(rc, "gradient of a linear layer of " + num(d.M) + " rows, " + num(d.K) + " to " + num(d.C));
+  Tensor work;
+  if (bytes) work = make({bytes}, d.x, at::kByte);
+  run(d.x, [&](pgemm_handle_t h) {
+    return pgemm_dense_backward(h, ptr(dy), dy.stride(0), ptr(d.x), d.x.stride(0), ptr(d.w), d.w.stride(0), slope ? ptr(z) : nullptr,
+                                dx ? ptr(*dx) : nullptr, dw ? ptr(*dw) : nullptr, db ? ptr(*db) : nullptr, d.M, d.N, d.K,
+                                nk ? PGEMM_B_NK : PGEMM_B_KN, act, gated, dtype_of(d.x, "x"), bytes ? ptr(work) : nullptr, bytes);
+  });
+  return {dx, dw, db};
+}
+
 } // namespace
 
 PYBIND11_MODULE(_ops, m) {
@@ -341,4 +438,6 @@ PYBIND11_MODULE(_ops, m) {
   m.def("grouped", &grouped);
   m.def("grouped_backward", &grouped_backward);
   m.def("w4", &w4);
+  m.def("dense", &dense);
+  m.def("dense_backward", &dense_backward);
 }

@@ -1,0 +1,152 @@
+// The linear layer: products of rows with one matrix, with what follows them
+// in the epilogue, and the gradients.
+//   z = x W + bias                      W: [K, C] ("K x N") or transposed, [C, K] ("N x K")
+//   y = act(z) + residual               C = N
+//   y = act(z[:, :N]) * z[:, N:] + residual   gated: C = 2N, gate columns first
+//   dz = dy * act'(z)                   gated: dy * up * act'(gate) and dy * act(gate)
+//   dbias = column sums of dz,  dx = dz W^T,  dW = x^T dz (or its transpose)
+// Sums, activations and column sums are fp32; z, dz and the outputs are
+// rounded once to the operands' 16 bits. (z is what the backward pass reads:
+// in 16 bits it costs act' less than the rounding of dz that follows, which
+// the matrix unit's operands need.)
+//
+// The products' bodies:
+//   few   (dense_few.h)    up to 32 rows: reading W bounds it
+//   tile  (dense_tile.h)   tiles of 128 (or 64) x 128, four LDS stages, whole or cut along the sum
+//   ping  (dense_pp.h)     256 x 256 ping-pong tiles for large products
+// tile and ping copy 16-byte chunks directly to LDS, so rows at other
+// addresses are first moved to padded rows in the workspace (one pass over
+// the operand; a body that loads odd rows itself runs at half the rate).
+#pragma once
+
+#include "dense_act.h"
+#include "gemm_fast.h"
+#include "moe_rows.h"
+
+namespace pgemm {
+namespace dense {
+
+using moe::u32x4;
+
+struct Args {
+  const uint16_t *a, *b; // rows of x and W; weight gradient: rows of both operands
+  int64_t lda, ldb;      // distance of two rows
+  int64_t half;          // gated: elements between a gate column's and its up column's first
+  uint16_t* c;           // [M][N], contiguous
+  uint16_t* z;           // pre-activations [M][N or 2N], or null
+  const uint16_t* bias;  // [N or 2N] or null
+  const uint16_t* residual; // rows ldr apart, or null
+  int64_t ldr;
+  int M, N, K; // rows and columns of c, length of the sum
+  int act;
+  int n_m, n_n; // tiles
+  int split;    // pieces the sum is cut into
+  float* part;  // split > 1: their sums [split][M][columns of part_ld()]
+};
+
+// Columns of a piece's row: gate and up halves each a multiple of 8.
+__host__ __device__ inline int64_t part_ld(const Args& a, bool gated) { return (int64_t)(gated ? 2 : 1) * ((a.N + 7) / 8 * 8); }
+
+// Eight elements of a row, those past its end zeros.
+__device__ inline u32x4 load8_upto(const uint16_t* row, int64_t n, int64_t N) {
+  return n + 8 <= N ? moe::load8<moe::kAnyAddress>(row + n) : moe::load_part(row + n, (int)(N - n));
+}
+
+// What follows the sums of eight columns n .. n+7 of row m (n < N): v the sums
+// (gated: of the gate), u those of up.
+template <int DT, bool GATED>
+struct Epilogue {
+  const Args& a;
+  const act::Consts k;
+  __device__ explicit Epilogue(const Args& a_) : a(a_), k(act::consts_of(a_.act)) {}
+
+  __device__ inline void bias_of(int n, float* bv, float* bu) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bv[i] = 0.0f;
+    if constexpr (GATED) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bu[i] = 0.0f;
+    }
+    if (!a.bias || n >= a.N) return;
+    moe::unpack<DT>(load8_upto(a.bias, n, a.N), bv);
+    if constexpr (GATED) moe::unpack<DT>(load8_upto(a.bias + a.N, n, a.N), bu);
+  }
+
+  __device__ inline void finish(int m, int n, float* v, float* u, const float* bv, const float* bu) const {
+    const int64_t N = a.N;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] += bv[i];
+      if constexpr (GATED) u[i] += bu[i];
+    }
+    if (a.z) {
+      uint16_t* z = a.z + (int64_t)m * (GATED ? 2 * N : N);
+      moe::store_row<moe::kAnyAddress>(z, n, (int)N, moe::pack<DT>(v));
+      if constexpr (GATED) moe::store_row<moe::kAnyAddress>(z + N, n, (int)N, moe::pack<DT>(u));
+    }
+    u32x4 res = {0, 0, 0, 0};
+    if (a.residual) res = load8_upto(a.residual + m * a.ldr, n, N);
+    act::with_path(k, [&](auto path) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = act::value<decltype(path)::value>(v[i], k);
+        if constexpr (GATED) v[i] *= u[i];
+      }
+    });
+    if (a.residual) {
+      float r[8];
+      moe::unpack<DT>(res, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    moe::store_row<moe::kAnyAddress>(a.c + (int64_t)m * N, n, (int)N, moe::pack<DT>(v));
+  }
+};
+
+// The step range of piece `piece`: first step and steps of 64.
+__device__ inline void piece_steps(int K, int split, int piece, int* first, int* count) {
+  const int steps = (K + 63) / 64;
+  const int lo = (int)((int64_t)steps * piece / split), hi = (int)((int64_t)steps * (piece + 1) / split);
+  *first = lo;
+  *count = hi - lo;
+}
+
+// Rows form: W as K x N or N x K; gradient form: c = a^T b over the rows of both.
+enum Form : int { kRowsKN = 0, kRowsNK = 1, kGrad = 2 };
+// kTile128 has four LDS stages and a CU to itself, kTile128Pair two stages, two workgroups to a CU.
+enum Body : int { kFew8, kFew16, kFew32, kTile64, kTile128, kTile128Pair, kPing };
+typedef void (*kernel_fn)(Args);
+
+// dz and the column sums of it (dense_rows.h).
+struct ActGradArgs {
+  const uint16_t* dy; // rows lddy apart
+  int64_t lddy;
+  const uint16_t* z;  // [M][C] contiguous (null for act none)
+  uint16_t* dz;       // null: only the sums are wanted
+  int64_t lddz;
+  float* part;        // null: no sums
+  uint16_t* db;
+  int M, N, act;
+  int stretches;
+};
+struct Kernels {
+  kernel_fn (*pick)(int body, int form, bool gated);
+  kernel_fn join[2];                 // by gated
+  void (*act_grad[2])(ActGradArgs);
+  void (*sum_columns)(ActGradArgs, int);
+};
+Kernels kernels_f16();
+Kernels kernels_bf16();
+
+// Rows of `halves` x `cols` elements, ld apart, to rows in which each half starts at a multiple of 8 and is
+// filled up with zeros.
+struct PadArgs {
+  const uint16_t* from;
+  int64_t ld;
+  uint16_t* to;
+  int rows, cols, halves;
+  int chunks; // of a half, eight elements each
+};
+
+} // namespace dense
+} // namespace pgemm

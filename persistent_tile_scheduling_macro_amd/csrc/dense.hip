@@ -1,0 +1,395 @@
+// Entry points of the linear layer.
+#include "context.h"
+#include "dense.h"
+
+using namespace pgemm;
+
+namespace {
+
+using dense::Args;
+
+constexpr int64_t kMaxSize = (int64_t)1 << 30;
+// Row strides up to which a tile's 32-bit offsets reach its last row (256 rows of 2-byte elements below 2^31).
+constexpr int64_t kMaxDirectStride = (int64_t)1 << 21;
+constexpr int kFewRows = 32; // up to so many, one pass over W
+
+// One chunk of eight a thread.
+__global__ void __launch_bounds__(256) pad_rows_kernel(dense::PadArgs p) {
+  const int per = p.chunks * p.halves;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / per;
+  if (r >= p.rows) return;
+  const int at = (int)(i - r * per), h = at >= p.chunks ? 1 : 0, c = 8 * (at - h * p.chunks);
+  const dense::u32x4 v = dense::load8_upto(p.from + r * p.ld + (int64_t)h * p.cols, c, p.cols);
+  *reinterpret_cast<dense::u32x4*>(p.to + 8 * i) = v;
+}
+
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// Scratch handed out piece by piece; with a null base it only counts.
+struct Scratch {
+  char* base;
+  int64_t used = 0;
+  template <class T>
+  T* take(int64_t count) {
+    const int64_t at = used;
+    used += (count * (int64_t)sizeof(T) + 255) / 256 * 256;
+    return base ? reinterpret_cast<T*>(base + at) : nullptr;
+  }
+};
+
+static_assert((int)dense::kFew8 == (int)PGEMM_DENSE_FEW8 && (int)dense::kFew16 == (int)PGEMM_DENSE_FEW16 && (int)dense::kFew32 == (int)PGEMM_DENSE_FEW32 &&
+                  (int)dense::kTile64 == (int)PGEMM_DENSE_TILE64 && (int)dense::kTile128 == (int)PGEMM_DENSE_TILE128 &&
+                  (int)dense::kTile128Pair == (int)PGEMM_DENSE_TILE128_PAIR && (int)dense::kPing == (int)PGEMM_DENSE_PINGPONG,
+              "the query's numbers are the bodies'");
+static_assert((int)act::kNone == (int)PGEMM_ACT_NONE && (int)act::kRelu == (int)PGEMM_ACT_RELU && (int)act::kGelu == (int)PGEMM_ACT_GELU &&
+                  (int)act::kGeluTanh == (int)PGEMM_ACT_GELU_TANH && (int)act::kSilu == (int)PGEMM_ACT_SILU,
+              "the header's numbers are the activations'");
+
+struct Plan { int body; int split; };
+
+struct Tile { int bm, bn; };
+Tile tile_of(int body) { return body == dense::kPing ? Tile{256, 256} : body == dense::kTile64 ? Tile{64, 128} : Tile{128, 128}; }
+
+// Body and pieces of a product of M x K with K x C (C columns before gating).
+Plan plan_rows(int64_t M, int64_t N, int64_t K, int form, bool gated) {
+  if (M <= kFewRows && (form == dense::kRowsNK || N >= 4))
+    return {M <= 8 ? dense::kFew8 : M <= 16 ? dense::kFew16 : dense::kFew32, 1};
+  const int64_t C = gated ? 2 * N : N;
+  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((C + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192) return {dense::kPing, 1};
+  const int body = M <= 64 ? dense::kTile64 : dense::kTile128;
+  const int64_t t = tiles(tile_of(body).bm, 128), steps = (K + 63) / 64;
+  int64_t split = t < 256 ? 256 / t : 1;
+  if (split > steps / 4) split = steps / 4 > 0 ? steps / 4 : 1;
+  if (split > 16) split = 16;
+  return {body, (int)split};
+}
+
+// The same for c [I][J] = a^T b over R rows.
+Plan plan_grad(int64_t R, int64_t I, int64_t J) {
+  auto tiles = [&](int bm) { return ((I + bm - 1) / bm) * ((J + bm - 1) / bm); };
+  if (tiles(256) >= 192 && R > 256) return {dense::kPing, 1};
+  const int64_t t = tiles(128), steps = (R + 63) / 64;
+  int64_t split = t < 256 && t > 0 ? 256 / t : 1;
+  if (split > steps / 4) split = steps / 4 > 0 ? steps / 4 : 1;
+  if (split > 16) split = 16;
+  return {steps <= 4 && t > 256 ? dense::kTile128Pair : dense::kTile128, (int)split};
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+
+// A matrix as an operand: rows at 16-byte addresses whose last chunk of eight may be read, or a copy that has them.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t half = 0; // elements from a row's first half to its second
+};
+bool direct(const void* p, int64_t ld, int64_t cols) {
+  return aligned16(p) && ld % 8 == 0 && cols % 8 == 0 && ld <= kMaxDirectStride;
+}
+
+struct Call {
+  pgemm_ctx* h; // null: only the scratch is counted
+  dense::Kernels kernels;
+  Scratch scratch;
+  hipError_t status = hipSuccess;
+
+  template <class K, class... A>
+  void launch(int64_t grid, int threads, K kernel, A... args) {
+    if (h && status == hipSuccess && grid > 0) status = enqueue(h->stream, dim3((unsigned)grid), dim3(threads), kernel, args...);
+  }
+
+  // wide: the rows can be used as they are.
+  Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int halves, bool wide) {
+    Operand o = {static_cast<const uint16_t*>(p), ld, cols};
+    if (wide) return o;
+    const int64_t padded = round8(cols), chunks = padded / 8 * halves;
+    uint16_t* to = scratch.take<uint16_t>(rows * padded * halves);
+    launch((rows * chunks + 255) / 256, 256, pad_rows_kernel,
+           dense::PadArgs{o.p, ld, to, (int)rows, (int)cols, halves, (int)(padded / 8)});
+    return {to, padded * halves, padded};
+  }
+
+  void product(Args a, Plan plan, int form, bool gated) {
+    const int64_t columns = gated ? 2 * (int64_t)a.N : a.N;
+    a.split = plan.split;
+    if (plan.split > 1) a.part = scratch.take<float>(plan.split * (int64_t)a.M * dense::part_ld(a, gated));
+    if (!h) return;
+    const dense::kernel_fn kernel = kernels.pick(plan.body, form, gated);
+    if (plan.body <= dense::kFew32) {
+      const int rows = plan.body == dense::kFew8 ? 8 : plan.body == dense::kFew16 ? 16 : 32;
+      const int wide = form == dense::kRowsNK ? 16 : 64;
+      if (status == hipSuccess)
+        status = enqueue(h->stream, dim3((unsigned)((a.N + wide - 1) / wide), (unsigned)((a.M + rows - 1) / rows)), dim3(512), kernel, a);
+      return;
+    }
+    const Tile t = tile_of(plan.body);
+    a.n_m = (int)((a.M + t.bm - 1) / t.bm);
+    a.n_n = (int)((columns + t.bn - 1) / t.bn);
+    const int64_t total = (int64_t)a.n_m * a.n_n * a.split;
+    if (plan.body == dense::kPing) launch(total < h->cus ? total : h->cus, 512, kernel, a);
+    else launch((total + 7) / 8 * 8, 512, kernel, a);
+    if (plan.split > 1)
+      launch(((int64_t)a.M * ((a.N + 7) / 8) + 255) / 256, 256, kernels.join[gated], a);
+  }
+};
+
+int check(pgemm_ctx* h, int64_t M, int64_t N, int64_t K, int layout, int act, int gated, int dtype) {
+  if (M < 0 || N < 0 || K < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "sizes M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+  if (layout != PGEMM_B_KN && layout != PGEMM_B_NK) return fail(h, PGEMM_ERR_INVALID_ARG, "unknown layout %d", layout);
+  if (act < 0 || act >= act::kActs) return fail(h, PGEMM_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (gated != 0 && gated != 1) return fail(h, PGEMM_ERR_INVALID_ARG, "gated is %d, not 0 or 1", gated);
+  if (dtype != PGEMM_F16 && dtype != PGEMM_BF16) return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
+  if (M > kMaxSize || N > kMaxSize || K > kMaxSize) return fail(h, PGEMM_ERR_UNSUPPORTED, "sizes must not exceed 2^30");
+  // tiles of 128 x 64 in one launch of 2^32 threads, in 16 pieces; rows that a tile's offsets span
+  const int64_t C = gated ? 2 * N : N;
+  auto tiles = [](int64_t a, int64_t b) { return ((a + 63) / 64) * ((b + 127) / 128); };
+  if (tiles(M, C) > (1 << 21) || tiles(M, K) > (1 << 21) || tiles(C, K) > (1 << 21) || C > kMaxDirectStride || K > kMaxDirectStride)
+    return fail(h, PGEMM_ERR_UNSUPPORTED, "M=%lld N=%lld K=%lld are more than one launch takes", (long long)M, (long long)N, (long long)K);
+  return PGEMM_OK;
+}
+
+int forward(Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, bool wide_x, bool wide_w, Args a, int layout, bool gated) {
+  const bool nk = layout == PGEMM_B_NK;
+  const int form = nk ? dense::kRowsNK : dense::kRowsKN;
+  const Plan plan = plan_rows(a.M, a.N, a.K, form, gated);
+  const int64_t columns = gated ? 2 * (int64_t)a.N : a.N;
+  if (plan.body <= dense::kFew32) {
+    a.a = static_cast<const uint16_t*>(x);
+    a.lda = ldx;
+    a.b = static_cast<const uint16_t*>(w);
+    a.ldb = ldw;
+    a.half = nk ? a.N * ldw : a.N;
+  } else {
+    const Operand xo = c.operand(x, ldx, a.M, a.K, 1, wide_x);
+    const Operand wo = nk ? c.operand(w, ldw, columns, a.K, 1, wide_w) : c.operand(w, ldw, a.K, a.N, gated ? 2 : 1, wide_w);
+    a.a = xo.p;
+    a.lda = xo.ld;
+    a.b = wo.p;
+    a.ldb = wo.ld;
+    a.half = nk ? a.N * wo.ld : wo.half;
+  }
+  c.product(a, plan, form, gated);
+  return PGEMM_OK;
+}
+
+// Stretches of the rows whose column sums are formed separately: enough workgroups to fill the card, 16 rows each at least.
+int stretches_of(int64_t M, int64_t N) {
+  const int64_t blocks = (N + 255) / 256;
+  int64_t s = 1024 / (blocks > 0 ? blocks : 1), most = (M + 15) / 16;
+  if (s < 1) s = 1;
+  if (s > most) s = most > 0 ? most : 1;
+  return (int)(s > 512 ? 512 : s);
+}
+
+struct Gradients {
+  const void *dy, *x, *w, *z;
+  int64_t lddy, ldx, ldw;
+  void *dx, *dw, *db;
+  int64_t M, N, K;
+  int layout, act;
+  bool gated;
+  bool wide_dy, wide_x, wide_w; // whether the rows can be used as they are
+  bool need_dx, need_dw, need_db;
+};
+
+void backward(Call& c, const Gradients& g) {
+  const int64_t C = g.gated ? 2 * g.N : g.N;
+  const bool nk = g.layout == PGEMM_B_NK, slope = g.act != act::kNone || g.gated;
+  const bool products = (g.need_dx || g.need_dw) && g.K > 0;
+  Operand dz = {static_cast<const uint16_t*>(g.dy), g.lddy};
+  const bool write = products && (slope || !g.wide_dy);
+  if (write || g.need_db) {
+    dense::ActGradArgs a = {};
+    a.dy = dz.p;
+    a.lddy = g.lddy;
+    a.z = slope ? static_cast<const uint16_t*>(g.z) : nullptr;
+    a.lddz = round8(C);
+    if (write) {
+      a.dz = c.scratch.take<uint16_t>(g.M * a.lddz);
+      dz = {a.dz, a.lddz};
+    }
+    a.M = (int)g.M;
+    a.N = (int)g.N;
+    a.act = g.act;
+    a.stretches = stretches_of(g.M, g.N);
+    a.db = static_cast<uint16_t*>(g.db);
+    if (g.need_db) a.part = c.scratch.take<float>(a.stretches * C);
+    if (c.h && c.status == hipSuccess && g.N > 0)
+      c.status = enqueue(c.h->stream, dim3((unsigned)((g.N + 255) / 256), (unsigned)a.stretches), dim3(256), c.kernels.act_grad[g.gated], a);
+    if (g.need_db) c.launch((C + 63) / 64, 256, c.kernels.sum_columns, a, (int)C);
+  }
+  if (!products) return;
+  if (g.need_dx) { // dz [M, C] times W: the sum runs over W's columns
+    const int form = nk ? dense::kRowsKN : dense::kRowsNK;
+    const Plan plan = plan_rows(g.M, g.K, C, form, false);
+    Operand w = {static_cast<const uint16_t*>(g.w), g.ldw};
+    if (plan.body > dense::kFew32) w = nk ? c.operand(g.w, g.ldw, C, g.K, 1, g.wide_w) : c.operand(g.w, g.ldw, g.K, C, 1, g.wide_w);
+    Args a = {};
+    a.a = dz.p;
+    a.lda = dz.ld;
+    a.b = w.p;
+    a.ldb = w.ld;
+    a.c = static_cast<uint16_t*>(g.dx);
+    a.M = (int)g.M;
+    a.N = (int)g.K;
+    a.K = (int)C;
+    c.product(a, plan, form, false);
+  }
+  if (g.need_dw) {
+    const Operand x = c.operand(g.x, g.ldx, g.M, g.K, 1, g.wide_x);
+    Args a = {};
+    a.a = nk ? dz.p : x.p;
+    a.lda = nk ? dz.ld : x.ld;
+    a.b = nk ? x.p : dz.p;
+    a.ldb = nk ? x.ld : dz.ld;
+    a.c = static_cast<uint16_t*>(g.dw);
+    a.M = (int)(nk ? C : g.K);
+    a.N = (int)(nk ? g.K : C);
+    a.K = (int)g.M;
+    c.product(a, plan_grad(g.M, a.M, a.N), dense::kGrad, false);
+  }
+}
+
+int short_of(pgemm_ctx* h, int64_t need, const void* work, int64_t have) {
+  if (have < need || (need && (!work || !aligned16(work))))
+    return fail(h, PGEMM_ERR_INVALID_ARG, "workspace of %lld bytes at %p, %lld at a multiple of 16 are needed", (long long)have, work,
+                (long long)need);
+  return PGEMM_OK;
+}
+
+dense::Kernels kernels_of(int dtype) { return dtype == PGEMM_F16 ? dense::kernels_f16() : dense::kernels_bf16(); }
+
+} // namespace
+
+extern "C" {
+
+int pgemm_dense_workspace(int64_t M, int64_t N, int64_t K, int layout, int gated, int wide, int64_t* bytes) {
+  if (!bytes) return PGEMM_ERR_INVALID_ARG;
+  *bytes = 0;
+  const int rc = check(nullptr, M, N, K, layout, 0, gated, PGEMM_F16);
+  if (rc != PGEMM_OK || M == 0 || N == 0) return rc;
+  Call c = {nullptr, {}, {nullptr}};
+  Args a = {};
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  const bool kn = layout == PGEMM_B_KN;
+  forward(c, nullptr, K, nullptr, 0, wide && K % 8 == 0, wide && (kn ? N : K) % 8 == 0, a, layout, gated);
+  *bytes = c.scratch.used;
+  return PGEMM_OK;
+}
+
+int pgemm_dense_run(pgemm_handle_t h, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                    const void* residual, int64_t ldr, void* y, void* z, int64_t M, int64_t N, int64_t K, int layout, int act,
+                    int gated, int dtype, void* work, int64_t work_bytes) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  int rc = check(h, M, N, K, layout, act, gated, dtype);
+  if (rc != PGEMM_OK) return rc;
+  const bool nk = layout == PGEMM_B_NK;
+  if (ldx < 0 || ldr < 0 || ldw < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "row strides %lld, %lld, %lld", (long long)ldx, (long long)ldw, (long long)ldr);
+  if (M == 0 || N == 0) return PGEMM_OK;
+  if (!y || (K > 0 && (!x || !w))) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  Args a = {};
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = ldr;
+  a.c = static_cast<uint16_t*>(y);
+  a.z = static_cast<uint16_t*>(z);
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.act = act;
+  const bool wide_x = direct(x, ldx, K), wide_w = direct(w, ldw, nk ? K : N);
+  Call count = {nullptr, {}, {nullptr}};
+  forward(count, x, ldx, w, ldw, wide_x, wide_w, a, layout, gated);
+  rc = short_of(h, count.scratch.used, work, work_bytes);
+  if (rc != PGEMM_OK) return rc;
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  Call c = {h, kernels_of(dtype), {static_cast<char*>(work)}};
+  forward(c, x, ldx, w, ldw, wide_x, wide_w, a, layout, gated);
+  return launch_status(h, c.status, "linear layer");
+}
+
+int pgemm_dense_backward_workspace(int64_t M, int64_t N, int64_t K, int layout, int act, int gated, int needs, int wide,
+                                   int64_t* bytes) {
+  if (!bytes || needs < 0 || needs > 7) return PGEMM_ERR_INVALID_ARG;
+  *bytes = 0;
+  const int rc = check(nullptr, M, N, K, layout, act, gated, PGEMM_F16);
+  if (rc != PGEMM_OK) return rc;
+  Call c = {nullptr, {}, {nullptr}};
+  Gradients g = {};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.layout = layout;
+  g.act = act;
+  g.gated = gated;
+  const int64_t columns = gated ? 2 * N : N;
+  g.wide_dy = wide && N % 8 == 0;
+  g.wide_x = wide && K % 8 == 0;
+  g.wide_w = wide && (layout == PGEMM_B_NK ? K : columns) % 8 == 0;
+  g.need_dx = needs & PGEMM_DENSE_DX;
+  g.need_dw = needs & PGEMM_DENSE_DW;
+  g.need_db = needs & PGEMM_DENSE_DB;
+  backward(c, g);
+  *bytes = c.scratch.used;
+  return PGEMM_OK;
+}
+
+int pgemm_dense_backward(pgemm_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                         const void* z, void* dx, void* dw, void* db, int64_t M, int64_t N, int64_t K, int layout, int act,
+                         int gated, int dtype, void* work, int64_t work_bytes) {
+  if (!h) return PGEMM_ERR_INVALID_ARG;
+  h->last_error[0] = 0;
+  int rc = check(h, M, N, K, layout, act, gated, dtype);
+  if (rc != PGEMM_OK) return rc;
+  if (lddy < 0 || ldx < 0 || ldw < 0)
+    return fail(h, PGEMM_ERR_INVALID_ARG, "row strides %lld, %lld, %lld", (long long)lddy, (long long)ldx, (long long)ldw);
+  const bool slope = act != act::kNone || gated, sums = M > 0 && N > 0;
+  if (sums && (dx || dw || db) && (!dy || (slope && !z))) return fail(h, PGEMM_ERR_INVALID_ARG, "dy or z is NULL");
+  if (sums && K > 0 && ((dx && !w) || (dw && !x))) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
+  const int64_t columns = gated ? 2 * N : N;
+  Gradients g = {dy, x, w, z, lddy, ldx, ldw, dx, dw, db, M, N, K, layout, act, gated != 0};
+  g.wide_dy = direct(dy, lddy, N);
+  g.wide_x = direct(x, ldx, K);
+  g.wide_w = direct(w, ldw, layout == PGEMM_B_NK ? K : columns);
+  g.need_dx = dx && M > 0;
+  g.need_dw = dw && N > 0;
+  g.need_db = db && N > 0;
+  Call count = {nullptr, {}, {nullptr}};
+  backward(count, g);
+  rc = short_of(h, count.scratch.used, work, work_bytes);
+  if (rc != PGEMM_OK) return rc;
+  DeviceScope dev(h->device);
+  if (!dev.ok()) return fail(h, PGEMM_ERR_HIP, "hipSetDevice failed");
+  Call c = {h, kernels_of(dtype), {static_cast<char*>(work)}};
+  backward(c, g);
+  return launch_status(h, c.status, "linear layer's gradient");
+}
+
+int pgemm_dense_query(int64_t M, int64_t N, int64_t K, int layout, int gated, int* body, int* pieces) {
+  if (!body || !pieces || M < 1 || N < 1 || K < 1) return PGEMM_ERR_INVALID_ARG;
+  const int rc = check(nullptr, M, N, K, layout, 0, gated, PGEMM_F16);
+  if (rc != PGEMM_OK) return rc;
+  const Plan p = plan_rows(M, N, K, layout == PGEMM_B_NK ? dense::kRowsNK : dense::kRowsKN, gated);
+  *body = p.body;
+  *pieces = p.split;
+  return PGEMM_OK;
+}
+
+int pgemm_dense_weight_grad_query(int64_t R, int64_t I, int64_t J, int* body, int* pieces) {
+  if (!body || !pieces || R < 1 || I < 1 || J < 1) return PGEMM_ERR_INVALID_ARG;
+  const int rc = check(nullptr, R, I, J, PGEMM_B_NK, 0, 0, PGEMM_F16);
+  if (rc != PGEMM_OK) return rc;
+  const Plan p = plan_grad(R, I, J);
+  *body = p.body;
+  *pieces = p.split;
+  return PGEMM_OK;
+}
+
+} // extern "C"

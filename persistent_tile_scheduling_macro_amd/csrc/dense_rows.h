@@ -1,0 +1,139 @@
+// What stands around the linear layer's products: the pieces' sums joined, dz
+// with the bias' column sums.
+#pragma once
+
+#include "dense.h"
+
+namespace pgemm {
+namespace dense {
+
+// c = epilogue(sum of the pieces' sums), eight columns a thread, pieces in order.
+template <int DT, bool GATED>
+__global__ void __launch_bounds__(256) join_kernel(Args a) {
+  const int chunks = (a.N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / chunks;
+  if (m >= a.M) return;
+  const int n = (int)(i - m * chunks) * 8;
+  const int64_t ld = part_ld(a, GATED), stride = a.M * ld;
+  const float* p = a.part + m * ld + n;
+  const Epilogue<DT, GATED> epilogue(a);
+  float bv[8], bu[8];
+  epilogue.bias_of(n, bv, bu);
+  floatx4_t s[GATED ? 4 : 2];
+#pragma unroll
+  for (int j = 0; j < (GATED ? 4 : 2); ++j) s[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int o = 0; o < a.split; ++o) {
+    const float* r = p + o * stride;
+    s[0] += *reinterpret_cast<const floatx4_t*>(r);
+    s[1] += *reinterpret_cast<const floatx4_t*>(r + 4);
+    if constexpr (GATED) {
+      s[2] += *reinterpret_cast<const floatx4_t*>(r + ld / 2);
+      s[3] += *reinterpret_cast<const floatx4_t*>(r + ld / 2 + 4);
+    }
+  }
+  float v[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = s[j / 4][j % 4];
+    if constexpr (GATED) u[j] = s[2 + j / 4][j % 4];
+  }
+  epilogue.finish((int)m, n, v, u, bv, bu);
+}
+
+// dz and the column sums of it. A workgroup takes 256 columns of y and a
+// stretch of the rows, a thread eight columns and every eighth row; the
+// threads' sums meet in LDS, the stretches' in `part` [stretches][C], which
+// sum_columns_kernel adds in order. dz rows are ldz apart (a multiple of 8),
+// filled up with zeros: they are the operands of the two products that follow.
+template <int DT, bool GATED>
+__global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
+  __shared__ float sums[8][GATED ? 2 : 1][256];
+  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  const int n = blockIdx.x * 256 + 8 * lane;
+  const int64_t C = GATED ? 2 * (int64_t)a.N : a.N;
+  const int lo = (int)((int64_t)a.M * blockIdx.y / a.stretches), hi = (int)((int64_t)a.M * (blockIdx.y + 1) / a.stretches);
+  const act::Consts k = act::consts_of(a.act);
+  const bool live = n < a.N;
+  float sv[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.0f;
+  if (live) {
+    act::with_path(k, [&](auto path) __attribute__((always_inline)) {
+      constexpr int PATH = decltype(path)::value;
+#pragma unroll 2
+      for (int m = lo + strip; m < hi; m += 8) {
+        float d[8], v[8], u[8];
+        moe::unpack<DT>(load8_upto(a.dy + m * a.lddy, n, a.N), d);
+        if (a.z) {
+          moe::unpack<DT>(load8_upto(a.z + m * C, n, a.N), v);
+          if constexpr (GATED) moe::unpack<DT>(load8_upto(a.z + m * C + a.N, n, a.N), u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float slope;
+            const float value = act::value_and_slope<PATH>(v[i], k, &slope);
+            if constexpr (GATED) {
+              v[i] = d[i] * u[i] * slope;
+              u[i] = d[i] * value;
+            } else {
+              v[i] = d[i] * slope;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = d[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sv[i] += v[i];
+          if constexpr (GATED) su[i] += u[i];
+        }
+        if (a.dz) {
+          uint16_t* to = a.dz + m * a.lddz;
+          moe::store_row<moe::kAnyAddress>(to, n, a.N, moe::pack<DT>(v));
+          if constexpr (GATED) moe::store_row<moe::kAnyAddress>(to + a.N, n, a.N, moe::pack<DT>(u));
+          if (n + 8 >= a.N) // the row's last thread fills it up
+            for (int64_t j = C; j < a.lddz; ++j) to[j] = 0;
+        }
+      }
+    });
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sums[strip][0][8 * lane + i] = sv[i];
+    if constexpr (GATED) sums[strip][1][8 * lane + i] = su[i];
+  }
+  __syncthreads();
+  const int col = blockIdx.x * 256 + tid;
+  if (col >= a.N) return;
+#pragma unroll
+  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += sums[j][h][tid];
+    a.part[(int64_t)blockIdx.y * C + (int64_t)h * a.N + col] = t;
+  }
+}
+
+// db = the stretches' sums, four threads a column.
+template <int DT>
+__global__ void __launch_bounds__(256) sum_columns_kernel(ActGradArgs a, int C) {
+  typedef typename Traits<DT>::out_t out_t;
+  __shared__ float sums[4][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
+  float t = 0.0f;
+  if (col < C) {
+#pragma unroll 4
+    for (int j = part; j < a.stretches; j += 4) t += a.part[(int64_t)j * C + col];
+  }
+  sums[part][threadIdx.x & 63] = t;
+  __syncthreads();
+  if (part || col >= C) return;
+  const int i = threadIdx.x;
+  t = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+  a.db[col] = __builtin_bit_cast(uint16_t, to_out(t, (out_t*)nullptr));
+}
+
+} // namespace dense
+} // namespace pgemm
