@@ -625,6 +625,54 @@ int pgemm_dense_query(int64_t M, int64_t N, int64_t K, int layout, int gated, in
 /* The same for the gradient of W: [I, J] = a^T b over R rows. */
 int pgemm_dense_weight_grad_query(int64_t R, int64_t I, int64_t J, int* body, int* pieces);
 
+/* ---- the router, and a routed layer of few tokens ----------------------- */
+
+/* Type of the router's logits. */
+typedef enum { PGEMM_LOGITS_F16 = 0, PGEMM_LOGITS_BF16 = 1, PGEMM_LOGITS_F32 = 3 } pgemm_logits_t;
+
+/* Scores: softmax over the experts, or each logit's sigmoid. */
+typedef enum { PGEMM_SCORE_SOFTMAX = 0, PGEMM_SCORE_SIGMOID = 1 } pgemm_score_t;
+
+/* Enqueue the choice of each token's k experts: ids[t] the k largest of the
+ * token's E logits, largest first and the first of equal ones first, weights[t]
+ * their scores, with `normalize` divided by the chosen scores' sum. Logits of
+ * -inf or NaN are never chosen (their scores are 0); where a token has fewer
+ * than k others, the places left get the id -1 and the weight 0, which
+ * pgemm_moe_dispatch drops. A logit of +inf gives NaN weights.
+ *   logits: T rows of E, ld apart; ids int32 and weights fp32: [T, k].
+ * All sums and exponentials are fp32. PGEMM_ERR_INVALID_ARG for a NULL handle
+ * or pointer, a negative size, E < 1, k outside [1, E], an unknown type or
+ * score; PGEMM_ERR_UNSUPPORTED for T above 2^24, E above 1024 or k above 64. */
+int pgemm_moe_route(pgemm_handle_t h, const void* logits, int64_t ld, int type, int64_t T, int64_t E, int64_t k, int score,
+                    int normalize, int32_t* ids, float* weights);
+
+/* Its gradient: dlogits [T, E], of the logits' type, from the gradient of the
+ * weights [T, k], with the call's logits, ids and weights. Places with an id
+ * outside [0, E) have none, whatever their dweights hold. */
+int pgemm_moe_route_backward(pgemm_handle_t h, const float* dweights, const void* logits, int64_t ld, int type,
+                             const int32_t* ids, const float* weights, int64_t T, int64_t E, int64_t k, int score,
+                             int normalize, void* dlogits);
+
+/* Enqueue a whole routed layer for few tokens, two launches for each 64:
+ *   out[t] = sum over j of weights[t, j] * (a(x[t]) W_out[e]^T), e = ids[t, j],
+ *   a(x) = act(x W_in[e]^T), gated: act of its first I columns times the others.
+ *   x: T rows of H, ldx apart; ids: [T, k] contiguous (outside [0, E): dropped;
+ *   an expert named twice counts twice); weights: fp32 [T, k]; w_in: [E, I, H],
+ *   gated [E, 2I, H]; w_out: [E, H, I]; out: [T, H].
+ * Only the experts that a token names are read, once for each 64 tokens. Sums
+ * are fp32 in a fixed order; a(x) and out are rounded once. `work` as for the
+ * linear layer; nothing is allocated. dtype is PGEMM_F16 or PGEMM_BF16.
+ * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
+ * k < 1, E < 1, an unknown type or activation or too small a workspace;
+ * PGEMM_ERR_UNSUPPORTED for T above 4096, k above 32, E above 1024, H above
+ * 2^20 or I above 2^19. */
+int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* ids, int ids_type, const float* weights,
+                    const void* w_in, const void* w_out, void* out, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I,
+                    int act, int gated, int dtype, void* work, int64_t work_bytes);
+
+/* Bytes of scratch that it needs. A pure function. */
+int pgemm_moe_layer_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t* bytes);
+
 /* Benchmark aid, not part of the GEMM: make about `n_cus` CUs of device
  * `device` unavailable for about `microseconds`, asynchronously on the HIP
  * stream `hip_stream` (NULL = null stream). It launches n_cus workgroups

@@ -52,6 +52,13 @@ PGEMM_GROUPED_FEW_GRAD = 5
 PGEMM_W4_INT4 = 0
 PGEMM_W4_E2M1 = 1
 
+PGEMM_LOGITS_F16 = 0
+PGEMM_LOGITS_BF16 = 1
+PGEMM_LOGITS_F32 = 3
+
+PGEMM_SCORE_SOFTMAX = 0
+PGEMM_SCORE_SIGMOID = 1
+
 PGEMM_ACT_NONE = 0
 PGEMM_ACT_RELU = 1
 PGEMM_ACT_GELU = 2
@@ -161,6 +168,11 @@ _dense_backward_workspace = _sig("pgemm_dense_backward_workspace", _int, _i64, _
                                  ctypes.POINTER(_i64))
 _dense_query = _sig("pgemm_dense_query", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
 _dense_weight_grad_query = _sig("pgemm_dense_weight_grad_query", _int, _i64, _i64, _i64, _ip, _ip)
+_moe_route = _sig("pgemm_moe_route", _int, _vp, _vp, _i64, _int, _i64, _i64, _i64, _int, _int, _vp, _vp)
+_moe_route_backward = _sig("pgemm_moe_route_backward", _int, _vp, _vp, _vp, _i64, _int, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp)
+_moe_layer = _sig("pgemm_moe_layer", _int, _vp, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _int,
+                  _int, _vp, _i64)
+_moe_layer_workspace = _sig("pgemm_moe_layer_workspace", _int, _i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64))
 _hold_cus = _sig("pgemm_hold_cus", _int, _vp, _int, _int, _int)
 
 
@@ -374,6 +386,32 @@ def pgemm_dense_weight_grad_query(R: int, I: int, J: int) -> tuple:
     body, pieces = ctypes.c_int(), ctypes.c_int()
     _check(_dense_weight_grad_query(R, I, J, ctypes.byref(body), ctypes.byref(pieces)))
     return body.value, pieces.value
+
+
+def pgemm_moe_route(h, logits, ld: int, type: int, T: int, E: int, k: int, score: int, normalize: int, ids, weights) -> None:
+    """Enqueue the choice of each token's k experts and their weights."""
+    _check(_moe_route(h, _ptr(logits), ld, type, T, E, k, score, normalize, _ptr(ids), _ptr(weights)), h)
+
+
+def pgemm_moe_route_backward(h, dweights, logits, ld: int, type: int, ids, weights, T: int, E: int, k: int, score: int,
+                             normalize: int, dlogits) -> None:
+    """Enqueue the gradient of the logits."""
+    _check(_moe_route_backward(h, _ptr(dweights), _ptr(logits), ld, type, _ptr(ids), _ptr(weights), T, E, k, score, normalize,
+                               _ptr(dlogits)), h)
+
+
+def pgemm_moe_layer(h, x, ldx: int, ids, ids_type: int, weights, w_in, w_out, out, T: int, k: int, E: int, H: int, I: int, act: int,
+                    gated: int, dtype: int, work=None, work_bytes: int = 0) -> None:
+    """Enqueue a whole routed layer of few tokens."""
+    _check(_moe_layer(h, _ptr(x), ldx, _ptr(ids), ids_type, _ptr(weights), _ptr(w_in), _ptr(w_out), _ptr(out), T, k, E, H, I, act,
+                      gated, dtype, _ptr(work) or None, work_bytes), h)
+
+
+def pgemm_moe_layer_workspace(T: int, k: int, E: int, H: int, I: int) -> int:
+    """Bytes of device scratch that pgemm_moe_layer needs."""
+    v = _i64()
+    _check(_moe_layer_workspace(T, k, E, H, I, ctypes.byref(v)))
+    return v.value
 
 
 def pgemm_hold_cus(stream, device: int, n_cus: int, microseconds: int) -> None:

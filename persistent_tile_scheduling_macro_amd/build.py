@@ -32,7 +32,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["pgemm.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f8.hip", "kernels_pp_f16.hip",
            "kernels_pp_bf16.hip", "kernels_pp_f8.hip", "kernels_pw_f16.hip", "kernels_pw_bf16.hip", "kernels_pw_f8.hip",
            "hold.hip", "moe.hip", "grouped.hip", "grouped_f16.hip", "grouped_bf16.hip", "w4.hip", "w4_f16.hip",
-           "w4_bf16.hip", "dense.hip", "dense_f16.hip", "dense_bf16.hip"]
+           "w4_bf16.hip", "dense.hip", "dense_f16.hip", "dense_bf16.hip", "route.hip", "layer.hip",
+           "layer_f16.hip", "layer_bf16.hip"]
 ARCH = os.environ.get("PGEMM_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

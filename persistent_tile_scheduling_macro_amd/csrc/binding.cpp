@@ -428,6 +428,92 @@ std::tuple<Maybe, Maybe, Maybe> dense_backward(const Tensor& dy_, const Tensor& 
   return {dx, dw, db};
 }
 
+// ------------------------------------------------- the router, the layer of few tokens
+int logits_type(const Tensor& t) {
+  if (t.scalar_type() == at::kFloat) return PGEMM_LOGITS_F32;
+  if (t.scalar_type() == at::kBFloat16) return PGEMM_LOGITS_BF16;
+  if (t.scalar_type() == at::kHalf) return PGEMM_LOGITS_F16;
+  type(join({"logits are ", c10::toString(t.scalar_type()), ", not float32, bfloat16 or float16"}));
+}
+Tensor check_logits(const char* name, const Tensor& t, int64_t k) {
+  logits_type(t);
+  no_tangent(t, "logits");
+  if (t.dim() != 2 || t.size(1) < 1) value(join({name, ": logits have shape ", shape(t), ", not [T, E]"}));
+  if (k < 1 || k > t.size(1)) value(join({name, ": k is ", num(k), " for ", num(t.size(1)), " experts"}));
+  return t.stride(1) == 1 || t.size(1) <= 1 ? t : t.contiguous();
+}
+
+std::tuple<Tensor, Tensor> route(const Tensor& logits_, int64_t k, int score, bool normalize) {
+  const Tensor l = check_logits("route", logits_, k);
+  on_device("route", {&l});
+  const int64_t T = l.size(0);
+  const Tensor ids = make({T, k}, l, at::kInt), weights = make({T, k}, l, at::kFloat);
+  run(l, [&](pgemm_handle_t h) {
+    return pgemm_moe_route(h, ptr(l), l.stride(0), logits_type(l), T, l.size(1), k, score, normalize, ptr<int32_t>(ids),
+                           ptr<float>(weights));
+  });
+  return {ids, weights};
+}
+
+// float32 [T, k], contiguous.
+Tensor per_choice(const char* name, const char* what, const Tensor& t, int64_t T, int64_t k) {
+  if (t.scalar_type() != at::kFloat) type(join({name, ": ", what, " are ", c10::toString(t.scalar_type()), ", not float32"}));
+  no_tangent(t, what);
+  if (t.dim() != 2 || t.size(0) != T || t.size(1) != k)
+    value(join({name, ": ", what, " have shape ", shape(t), ", not [", num(T), ", ", num(k), "]"}));
+  return t.contiguous();
+}
+
+Tensor route_backward(const Tensor& dweights_, const Tensor& logits_, const Tensor& ids_, const Tensor& weights_, int score,
+                      bool normalize) {
+  if (ids_.scalar_type() != at::kInt) type(join({"ids are ", c10::toString(ids_.scalar_type()), ", not int32"}));
+  if (ids_.dim() != 2) value(join({"ids have shape ", shape(ids_), ", not [T, k]"}));
+  const int64_t T = ids_.size(0), k = ids_.size(1);
+  const Tensor l = check_logits("route_backward", logits_, k);
+  if (l.size(0) != T) value(join({"route_backward: logits of ", num(l.size(0)), " tokens, ids of ", num(T)}));
+  const Tensor d = per_choice("route_backward", "dweights", dweights_, T, k), w = per_choice("route_backward", "weights", weights_, T, k);
+  on_device("route_backward", {&l, &ids_, &d, &w});
+  const Tensor ids = ids_.contiguous(), dl = make(l.sizes(), l, l.scalar_type());
+  run(l, [&](pgemm_handle_t h) {
+    return pgemm_moe_route_backward(h, ptr<float>(d), ptr(l), l.stride(0), logits_type(l), ptr<int32_t>(ids), ptr<float>(w), T,
+                                    l.size(1), k, score, normalize, ptr(dl));
+  });
+  return dl;
+}
+
+Tensor layer(const Tensor& x_, const Tensor& ids_, const Tensor& weights_, const Tensor& w_in_, const Tensor& w_out_, int act, bool gated) {
+  const char* name = "moe.layer";
+  const Tensor x = rows_of(x_, "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  if (ids_.scalar_type() != at::kInt && ids_.scalar_type() != at::kLong)
+    type(join({"ids are ", c10::toString(ids_.scalar_type()), ", not int32 or int64"}));
+  if (ids_.dim() != 2 || ids_.size(0) != T || ids_.size(1) < 1)
+    value(join({"ids have shape ", shape(ids_), ", not [", num(T), ", k]"}));
+  const int64_t k = ids_.size(1);
+  const Tensor weights = per_choice(name, "weights", weights_, T, k);
+  if (w_out_.dim() != 3 || w_out_.size(0) < 1 || w_out_.size(1) != H)
+    value(join({name, ": w_out has shape ", shape(w_out_), ", not [E, ", num(H), ", I]"}));
+  const int64_t E = w_out_.size(0), I = w_out_.size(2);
+  same_kind(name, "w_out", w_out_, x, {E, H, I});
+  same_kind(name, "w_in", w_in_, x, {E, gated ? 2 * I : I, H});
+  on_device(name, {&x, &ids_, &weights});
+  const Tensor ids = ids_.contiguous(), w_in = w_in_.contiguous(), w_out = w_out_.contiguous();
+  const Tensor out = make({T, H}, x, x.scalar_type());
+  int64_t bytes = 0;
+  const int rc = pgemm_moe_layer_workspace(T, k, E, H, I, &bytes);
+  if (rc != PGEMM_OK)
+    raise(rc, "layer of " + num(T) + " tokens, " + num(k) + " of " + num(E) + " experts, " + num(H) + " x " + num(I) +
+                  " (more than 4096 tokens go through dispatch, grouped_matmul and combine)");
+  Tensor work;
+  if (bytes) work = make({bytes}, x, at::kByte);
+  run(x, [&](pgemm_handle_t h) {
+    return pgemm_moe_layer(h, ptr(x), x.stride(0), ptr(ids), ids.scalar_type() == at::kInt ? PGEMM_IDS_I32 : PGEMM_IDS_I64,
+                           ptr<float>(weights), ptr(w_in), ptr(w_out), ptr(out), T, k, E, H, I, act, gated, dtype_of(x, "x"),
+                           bytes ? ptr(work) : nullptr, bytes);
+  });
+  return out;
+}
+
 } // namespace
 
 PYBIND11_MODULE(_ops, m) {
@@ -440,4 +526,7 @@ PYBIND11_MODULE(_ops, m) {
   m.def("w4", &w4);
   m.def("dense", &dense);
   m.def("dense_backward", &dense_backward);
+  m.def("route", &route);
+  m.def("route_backward", &route_backward);
+  m.def("layer", &layer);
 }

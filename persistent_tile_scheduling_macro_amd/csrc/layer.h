@@ -1,0 +1,399 @@
+// A whole routed layer for the few tokens of a decoding batch, in two launches:
+//   h[s] = act(x[t] W_in[e]^T)            gated: act(gate) * up of its 2I columns
+//   out[t] = sum over t's slots s of weights[s] * (h[s] W_out[e]^T)
+// with e = ids[s]. Reading the matrices of the experts that some token takes
+// bounds it; each is read once for up to 64 tokens.
+//
+// up_kernel: one workgroup for an awake expert (the a-th that some slot names:
+// found from a bitmap of the ids, so no sort and no launch before it) and 16
+// columns of h. Rows are the expert's tokens; the scheme is that of
+// dense_few.h. The first column's workgroups also write the plan that the
+// second launch reads: expert, slots, weights. A token that names an expert twice
+// is one row with the sum of its weights.
+//
+// down_kernel: one workgroup for 16 columns of out and all awake experts. The
+// experts' sums of I are laid end to end, in steps of 64, and cut evenly
+// between the waves, which read ahead across experts. At an expert's end a
+// wave adds its sums, times the rows' weights, in fp32 to its own [T][16] part of
+// LDS; the waves' parts are added in order. So no atomics, no row of any
+// expert's output goes through memory, and h is the only intermediate value that
+// is rounded (to 16 bits: it is an MFMA operand).
+#pragma once
+
+#include "dense.h"
+#include "grouped_few.h"
+
+namespace pgemm {
+namespace layer {
+
+using grouped::load_upto;
+using grouped::turn_at;
+using moe::u32x4;
+
+constexpr int kTokens = 64; // of one pass
+constexpr int kMaxSlots = 2048;
+
+struct Args {
+  const uint16_t* x; // rows ldx apart
+  int64_t ldx;
+  const void* ids;   // [T, k] contiguous, 32 or 64 bits
+  int ids64;
+  const float* weights;  // [T, k]
+  const uint16_t* w_in;  // [E][I or 2I][H]
+  const uint16_t* w_out; // [E][H][I]
+  uint16_t* h;           // [T * k][I]
+  int* awake;            // number of awake experts, then {expert | rows << 16} of each
+  int* slots;            // [awake][kTokens]
+  float* shares;         // [awake][kTokens]
+  uint16_t* out;         // [T, H]
+  int T, k, E, H, I, act;
+};
+
+__device__ inline void wave_fence() { // LDS serves a wave in order: only the compiler has to be held
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// MB: blocks of 16 rows that T tokens can need.
+template <int DT, bool GATED, int MB>
+__global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
+  constexpr int WAVES = 8, BLK = GATED ? 2 : 1, D = 2, XL = 2 * MB;
+  constexpr int TURN = 2048 * (MB + BLK), JOIN = BLK * MB * 1024;
+  typedef typename fast::Frag<DT>::t frag_t;
+  typedef typename Traits<DT>::out_t out_t;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * (TURN > JOIN ? TURN : JOIN)];
+  __shared__ short s_ids[kMaxSlots];
+  __shared__ unsigned s_awake[moe::kMaxExperts / 32];
+  __shared__ int s_row[kTokens];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, s = lane & 15;
+  const int n = a.T * a.k, H = a.H, I = a.I;
+
+  // ---- the awake expert of this workgroup and its rows
+  if (tid < moe::kMaxExperts / 32) s_awake[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += WAVES * 64) {
+    const int e = a.ids64 ? moe::key_of<int64_t>(a.ids, i, a.E) : moe::key_of<int32_t>(a.ids, i, a.E);
+    s_ids[i] = (short)e;
+    if (e < a.E) atomicOr(&s_awake[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  const unsigned word = lane < moe::kMaxExperts / 32 ? s_awake[lane] : 0;
+  int before = __popc(word);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up(before, d);
+    if (lane >= d) before += v;
+  }
+  const int which = blockIdx.y, awake = __builtin_amdgcn_readfirstlane(__shfl(before, 31));
+  const bool writes = blockIdx.x == 0;
+  if (writes && which == 0 && tid == 0) a.awake[0] = awake;
+  if (which >= awake) return;
+  const uint64_t hit = __ballot(lane < 32 && before > which);
+  const int at = (int)__builtin_ctzll(hit);
+  int skip = which - __builtin_amdgcn_readfirstlane(__shfl(before - __popc(word), at));
+  unsigned bits = __builtin_amdgcn_readfirstlane(__shfl((int)word, at));
+  for (; skip > 0; --skip) bits &= bits - 1;
+  const int e = 32 * at + __builtin_ctz(bits);
+
+  // every wave finds the rows for itself: lane t looks through its token's choices
+  int slot = -1;
+  float share = 0.0f;
+  if (lane < a.T) {
+    for (int j = a.k - 1; j >= 0; --j)
+      if (s_ids[lane * a.k + j] == e) slot = lane * a.k + j;
+    if (writes && wave == 0)
+      for (int j = 0; j < a.k; ++j)
+        if (s_ids[lane * a.k + j] == e) share += a.weights[lane * a.k + j];
+  }
+  const uint64_t taken = __ballot(slot >= 0);
+  const int rows = (int)__popcll(taken);
+  if (wave == 0 && slot >= 0) {
+    const int r = (int)__popcll(taken & ((1ull << lane) - 1));
+    s_row[r] = slot;
+    if (writes) {
+      a.slots[which * kTokens + r] = slot;
+      a.shares[which * kTokens + r] = share;
+    }
+  }
+  if (writes && tid == 0) a.awake[1 + which] = e | rows << 16;
+  __syncthreads();
+
+  // ---- the product
+  const int n0 = blockIdx.x * 16, row = lane >> 3, chunk = lane & 7;
+  const int x_loads = __builtin_amdgcn_readfirstlane((rows + 7) >> 3), blocks = (x_loads + 1) >> 1;
+  const uint16_t* x[XL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) x[i] = a.x + s_row[min(8 * i + row, rows - 1)] / a.k * a.ldx + 8 * chunk;
+  const uint16_t* w[BLK * 2];
+#pragma unroll
+  for (int i = 0; i < BLK * 2; ++i)
+    w[i] = a.w_in + ((int64_t)e * I * BLK + (i >= 2 ? I : 0) + min(n0 + 8 * (i & 1) + row, I - 1)) * H + 8 * chunk;
+  struct Slot { u32x4 x[XL], w[BLK * 2]; };
+  auto load = [&](Slot& t, int step) __attribute__((always_inline)) {
+    const int64_t k0 = (int64_t)step * 64;
+#pragma unroll
+    for (int i = 0; i < BLK * 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if (i < x_loads) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
+  };
+  floatx4_t acc[MB][BLK];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int c = 0; c < BLK; ++c) acc[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + 2048 * MB;
+  auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
+    wave_fence(); // the last step's reads come first
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if (i < x_loads) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
+#pragma unroll
+    for (int i = 0; i < BLK * 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
+    wave_fence();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      frag_t f[BLK];
+#pragma unroll
+      for (int c = 0; c < BLK; ++c) f[c] = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(16 * c + s, 4 * h + g));
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        if (b < blocks) {
+          // an odd number of loads leaves the block's upper half to repeat its lower one
+          const int r = 16 * b + (2 * b + 1 < x_loads ? s : s & 7);
+          const frag_t xf = *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(r, 4 * h + g));
+#pragma unroll
+          for (int c = 0; c < BLK; ++c) acc[b][c] = mfma(f[c], xf, acc[b][c]);
+        }
+    }
+  };
+  const int whole = H / 64, mine = (whole - wave + WAVES - 1) / WAVES;
+  if (mine > 0) {
+    auto step_of = [&](int i) __attribute__((always_inline)) { return wave + WAVES * min(i, mine - 1); };
+    Slot t[D];
+#pragma unroll
+    for (int j = 0; j < D; ++j) load(t[j], step_of(j));
+    for (int i = 0; i < mine; i += D) {
+#pragma unroll
+      for (int j = 0; j < D; ++j) {
+        if (i + j < mine) multiply(t[j]);
+        load(t[j], step_of(i + j + D)); // past the range the last one again, not used
+      }
+    }
+  }
+  if (whole * 64 < H && wave == whole % WAVES) { // the partial step, zeros past H
+    const int k0 = whole * 64;
+    Slot t;
+#pragma unroll
+    for (int i = 0; i < BLK * 2; ++i) t.w[i] = load_upto(w[i] + k0, H - k0 - 8 * chunk, H);
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if (i < x_loads) t.x[i] = load_upto(x[i] + k0, H - k0 - 8 * chunk, H);
+    multiply(t);
+  }
+
+  __syncthreads(); // every wave is through with its part of the LDS
+  floatx4_t* join = reinterpret_cast<floatx4_t*>(lds);
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int c = 0; c < BLK; ++c) join[(wave * BLK * MB + c * MB + b) * 64 + lane] = acc[b][c];
+  __syncthreads();
+  const int b = tid >> 6, m = 16 * b + s;
+  if (b >= MB || m >= rows) return;
+  floatx4_t v = join[tid], u = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int o = 1; o < WAVES; ++o) v += join[o * BLK * MB * 64 + tid];
+  if constexpr (GATED) {
+    u = join[MB * 64 + tid];
+#pragma unroll
+    for (int o = 1; o < WAVES; ++o) u += join[o * BLK * MB * 64 + MB * 64 + tid];
+  }
+  const act::Consts k = act::consts_of(a.act);
+  uint16_t* to = a.h + (int64_t)s_row[m] * I;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int c = n0 + 4 * g + r;
+    if (c >= I) continue;
+    float y = v[r];
+    act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
+    if constexpr (GATED) y *= u[r];
+    to[c] = __builtin_bit_cast(uint16_t, to_out(y, (out_t*)nullptr));
+  }
+}
+
+template <int DT, int MB>
+__global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
+  constexpr int WAVES = 8, D = MB == 1 ? 4 : 2, XL = 2 * MB, RING = 8;
+  static_assert(D < RING, "a ring entry lasts from an expert's first load to its last product");
+  constexpr int TURN = 2048 * (MB + 1), TOKENS = 16 * MB;
+  typedef typename fast::Frag<DT>::t frag_t;
+  typedef typename Traits<DT>::out_t out_t;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * TURN];
+  __shared__ floatx4_t s_out[WAVES][TOKENS * 4];     // [token][16 columns]
+  __shared__ int s_token[WAVES][RING][TOKENS];       // of an expert's rows
+  __shared__ float s_share[WAVES][RING][TOKENS];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, s = lane & 15, row = lane >> 3, chunk = lane & 7;
+  const int n0 = blockIdx.x * 16, H = a.H, I = a.I;
+  const int awake = __builtin_amdgcn_readfirstlane(a.awake[0]);
+  const int steps = (I + 63) / 64;
+  const int64_t units = (int64_t)awake * steps;
+  const int64_t from = units * wave / WAVES, to = units * (wave + 1) / WAVES;
+  for (int i = lane; i < TOKENS * 4; i += 64) s_out[wave][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+  // ---- the load cursor: expert, step, its rows' slots in the lanes, and the next expert's
+  int l_at = (int)(from / steps), l_step = (int)(from - (int64_t)l_at * steps);
+  int64_t left = to - from;
+  int next_info = 0, next_slot = 0;
+  float next_share = 0.0f;
+  auto fetch = [&](int at) __attribute__((always_inline)) {
+    const int i = min(at, awake - 1);
+    next_info = a.awake[1 + i];
+    next_slot = a.slots[i * kTokens + lane]; // lanes past the rows hold whatever is there
+    next_share = a.shares[i * kTokens + lane];
+  };
+  const uint16_t* w[2];
+  int x[XL], l_loads = 0; // element offsets in h
+  auto enter = [&]() __attribute__((always_inline)) { // expert l_at's rows come into use
+    const int info = __builtin_amdgcn_readfirstlane(next_info), e = info & 0xFFFF, rows = info >> 16;
+    const int slot = next_slot;
+    const float share = next_share;
+    if (lane < TOKENS) {
+      s_token[wave][l_at % RING][lane] = lane < rows ? slot / a.k : -1;
+      s_share[wave][l_at % RING][lane] = share;
+    }
+    l_loads = (rows + 7) >> 3;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) x[i] = __shfl(slot, min(8 * i + row, rows - 1)) * I + 8 * chunk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = a.w_out + ((int64_t)e * H + min(n0 + 8 * i + row, H - 1)) * I + 8 * chunk;
+    fetch(l_at + 1);
+  };
+  struct Slot { u32x4 x[XL], w[2]; };
+  auto load = [&](Slot& t) __attribute__((always_inline)) {
+    if (left <= 0) return;
+    --left;
+    const int k0 = l_step * 64;
+    if (k0 + 64 <= I) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i < l_loads) t.x[i] = moe::load8<moe::kAnyAddress>(a.h + x[i] + k0);
+    } else {
+      const int rest = I - k0 - 8 * chunk;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) t.w[i] = load_upto(w[i] + k0, rest, I);
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i < l_loads) t.x[i] = load_upto(a.h + x[i] + k0, rest, I);
+    }
+    if (++l_step == steps) {
+      l_step = 0;
+      ++l_at;
+      if (left > 0) enter();
+    }
+  };
+
+  // ---- the compute cursor
+  int c_at = l_at, c_step = l_step;
+  floatx4_t acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  auto flush = [&]() __attribute__((always_inline)) { // expert c_at's sums to their tokens
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int token = s_token[wave][c_at % RING][16 * b + s];
+      const float share = s_share[wave][c_at % RING][16 * b + s];
+      if (token >= 0) {
+        floatx4_t* o = &s_out[wave][token * 4 + g];
+        floatx4_t v = *o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(share, acc[b][r], v[r]);
+        *o = v;
+      }
+      acc[b] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + 2048 * MB;
+  auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
+    wave_fence(); // the last step's reads come first
+#pragma unroll
+    for (int i = 0; i < XL; ++i) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
+    wave_fence();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const frag_t f = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(s, 4 * h + g));
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        acc[b] = mfma(f, *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(16 * b + s, 4 * h + g)), acc[b]);
+    }
+    if (++c_step == steps) {
+      wave_fence();
+      flush();
+      c_step = 0;
+      ++c_at;
+    }
+  };
+  const int mine = (int)(to - from);
+  if (mine > 0) {
+    fetch(l_at);
+    enter();
+    Slot t[D];
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+#pragma unroll
+      for (int i = 0; i < XL; ++i) t[j].x[i] = u32x4{0, 0, 0, 0}; // rows that no load fills
+      load(t[j]);
+    }
+    for (int i = 0; i < mine; i += D) {
+#pragma unroll
+      for (int j = 0; j < D; ++j)
+        if (i + j < mine) {
+          multiply(t[j]);
+          load(t[j]);
+        }
+    }
+    if (c_step) {
+      wave_fence();
+      flush(); // the next wave has the rest of this expert's sum
+    }
+  }
+  __syncthreads();
+  const float* parts = reinterpret_cast<const float*>(s_out);
+  for (int i = tid; i < a.T * 16; i += WAVES * 64) {
+    const int c = n0 + (i & 15);
+    float v = parts[i];
+#pragma unroll
+    for (int o = 1; o < WAVES; ++o) v += parts[o * TOKENS * 16 + i];
+    if (c < H) a.out[(int64_t)(i >> 4) * H + c] = __builtin_bit_cast(uint16_t, to_out(v, (out_t*)nullptr));
+  }
+}
+
+typedef void (*kernel_fn)(Args);
+kernel_fn up_f16(bool gated, int blocks);
+kernel_fn up_bf16(bool gated, int blocks);
+kernel_fn down_f16(int blocks);
+kernel_fn down_bf16(int blocks);
+
+template <int DT>
+kernel_fn pick_up(bool gated, int blocks) {
+  if (blocks == 1) return gated ? up_kernel<DT, true, 1> : up_kernel<DT, false, 1>;
+  if (blocks == 2) return gated ? up_kernel<DT, true, 2> : up_kernel<DT, false, 2>;
+  return gated ? up_kernel<DT, true, 4> : up_kernel<DT, false, 4>;
+}
+template <int DT>
+kernel_fn pick_down(int blocks) {
+  return blocks == 1 ? down_kernel<DT, 1> : blocks == 2 ? down_kernel<DT, 2> : down_kernel<DT, 4>;
+}
+
+} // namespace layer
+} // namespace pgemm

@@ -1,0 +1,9 @@
+// The routed layer's kernels for bf16 operands.
+#include "layer.h"
+
+namespace pgemm {
+namespace layer {
+kernel_fn up_bf16(bool gated, int blocks) { return pick_up<kBF16>(gated, blocks); }
+kernel_fn down_bf16(int blocks) { return pick_down<kBF16>(blocks); }
+} // namespace layer
+} // namespace pgemm

@@ -1,0 +1,9 @@
+// The routed layer's kernels for f16 operands.
+#include "layer.h"
+
+namespace pgemm {
+namespace layer {
+kernel_fn up_f16(bool gated, int blocks) { return pick_up<kF16>(gated, blocks); }
+kernel_fn down_f16(int blocks) { return pick_down<kF16>(blocks); }
+} // namespace layer
+} // namespace pgemm

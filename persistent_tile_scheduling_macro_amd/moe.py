@@ -1,10 +1,15 @@
 """Mixture-of-experts operators: token rows to their experts, the experts' products, and back.
 
-A layer is three kinds of call::
+A layer is four kinds of call::
 
+    ids, weights = moe.route(logits, k)                        # each token's experts
     xs, plan = moe.dispatch(x, ids, E)                         # rows sorted by expert
     ys = moe.grouped_matmul(xs, w, plan.offsets, layout="nk")  # each row times its expert's matrix
     out = moe.combine(ys, weights, plan)                       # the token's rows, weighted and summed
+
+and for the few tokens of a decoding batch the last three are one::
+
+    out = moe.layer(x, ids, weights, w_in, w_out, act="silu", gated=True)
 
 Every step runs in the HIP kernels behind the C ABI (``pgemm_moe_*``, ``pgemm_grouped_*``); the binding checks shapes
 and types, makes the outputs and hands over pointers. The calls enqueue on torch's current stream and return without
@@ -20,7 +25,8 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _ops
+from . import PGEMM_SCORE_SIGMOID, PGEMM_SCORE_SOFTMAX, _ops
+from .dense import _act
 
 
 class RoutePlan:
@@ -38,6 +44,49 @@ class RoutePlan:
 
 def _records(a, b=None) -> bool:
     return (a.requires_grad or (b is not None and b.requires_grad)) and torch.is_grad_enabled()
+
+
+# ------------------------------------------------------------------ router
+_SCORES = {"softmax": PGEMM_SCORE_SOFTMAX, "sigmoid": PGEMM_SCORE_SIGMOID}
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(_SCORES)}")
+    return _SCORES[score]
+
+
+def route(logits, k: int, *, score: str = "softmax", normalize: bool = True):
+    """Each token's k experts and their weights: (ids int32 [T, k], weights float32 [T, k]).
+
+    logits [T, E], float32, bf16 or fp16. The largest are chosen, largest first, the first of equal ones first; -inf and
+    NaN never, and a token with fewer than k others gets ids of -1 with weights of 0 in the places left, which
+    ``dispatch`` drops. The weights are the chosen scores, the softmax over all experts or each logit's sigmoid; with
+    normalize they are divided by their sum. Differentiable in logits, through the weights.
+    """
+    if _records(logits):
+        return _Route.apply(logits, k, _score(score), bool(normalize))
+    return _ops.route(logits, k, _score(score), bool(normalize))
+
+
+def route_backward(dweights, logits, ids, weights, *, score: str = "softmax", normalize: bool = True):
+    """Gradient of logits [T, E] from the gradient of the weights [T, k], with what ``route`` took and returned."""
+    return _ops.route_backward(dweights, logits, ids, weights, _score(score), bool(normalize))
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, normalize):
+        ids, weights = _ops.route(logits, k, score, normalize)
+        ctx.save_for_backward(logits, ids, weights)
+        ctx.how = score, normalize
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, dweights):
+        return _ops.route_backward(dweights, *ctx.saved_tensors, *ctx.how), None, None, None
 
 
 # ---------------------------------------------------------------- dispatch
@@ -132,3 +181,17 @@ class _Grouped(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         return *_ops.grouped_backward(dy, *ctx.saved_tensors, ctx.nk, *ctx.needs_input_grad[:2]), None, None
+
+
+# --------------------------------------------------- a whole layer of few tokens
+def layer(x, ids, weights, w_in, w_out, *, act: str = "silu", gated: bool = True):
+    """out[t] = sum over j of weights[t, j] * (a(x[t]) @ w_out[e].T) with e = ids[t, j], in two launches for each 64 tokens.
+
+    x [T, H]; ids int32 or int64 [T, k] (outside [0, E): dropped); weights float32 [T, k]; a(x) = act(x @ w_in[e].T) with
+    w_in [E, I, H], or, gated, w_in [E, 2I, H] and act of the first I columns times the others; w_out [E, H, I]; act as
+    in ``dense.matmul``. Each expert that a token names is read once for 64 tokens, so it is for the few tokens of a
+    decoding batch; it takes up to 4096. For serving: it records no gradient, and refuses arguments that want one.
+    """
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, w_in, w_out)):
+        raise ValueError("moe.layer has no gradient: call it under torch.no_grad() or on detached tensors")
+    return _ops.layer(x, ids, weights, w_in, w_out, _act(act), gated)
