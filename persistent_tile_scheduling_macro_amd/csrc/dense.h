@@ -103,6 +103,28 @@ struct Epilogue {
   }
 };
 
+// Steps 0 .. n-1 with D of them in flight (two where there are fewer than D): load(slot, step) into registers,
+// multiply(slot). Loads past the last step are of that step again and not used: after a branch around a load the
+// compiler would wait for more than it has to.
+template <int D, class Slot, class L, class F>
+__device__ inline void stream_loop(int n, L load, F multiply) {
+  Slot t[D];
+#pragma unroll
+  for (int j = 0; j < D; ++j) load(t[j], min(j, n - 1));
+  for (int i = 0; i < n; i += D) {
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      if (i + j < n) multiply(t[j]);
+      load(t[j], min(i + j + D, n - 1));
+    }
+  }
+}
+template <int D, class Slot, class L, class F>
+__device__ inline void stream_steps(int n, L load, F multiply) {
+  if (n >= D) stream_loop<D, Slot>(n, load, multiply);
+  else if (n > 0) stream_loop<D < 2 ? D : 2, Slot>(n, load, multiply);
+}
+
 // The step range of piece `piece`: first step and steps of 64.
 __device__ inline void piece_steps(int K, int split, int piece, int* first, int* count) {
   const int steps = (K + 63) / 64;

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(WAVES * 64, BLK == 8 ? 2 : 4) few_kernel(Args 
   constexpr int STEP = NK ? 64 : 32, H = STEP / 32;
   constexpr int ROW = STEP * 2, LPR = ROW / 16, RPL = 64 / LPR; // bytes of a step's row, lanes to a row, rows of a load
   constexpr int L = 16 / RPL, XL = ROWS < 16 && RPL == 8 ? 1 : MB * L; // loads of 16 rows; loads of x
-  constexpr int D = 2;
+  constexpr int D = !NK || ROWS > 16 ? 2 : GATED ? 3 : 4; // steps in flight, as many as 128 registers hold
   constexpr int OUT = GATED ? BLK / 2 : BLK; // blocks of y's columns
   typedef typename fast::Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;
@@ -163,19 +163,7 @@ __global__ void __launch_bounds__(WAVES * 64, BLK == 8 ? 2 : 4) few_kernel(Args 
 
   const int whole = K / STEP;
   const int mine = (whole - wave + WAVES - 1) / WAVES; // steps wave, wave + WAVES, ... (none if not positive)
-  if (mine > 0) {
-    auto at = [&](int i) __attribute__((always_inline)) { return wave + WAVES * min(i, mine - 1); };
-    Slot t[D];
-#pragma unroll
-    for (int j = 0; j < D; ++j) load(t[j], at(j));
-    for (int i = 0; i < mine; i += D) {
-#pragma unroll
-      for (int j = 0; j < D; ++j) {
-        if (i + j < mine) multiply(t[j]);
-        load(t[j], at(i + j + D)); // past the range the last one again, not used
-      }
-    }
-  }
+  stream_steps<D, Slot>(mine, [&](Slot& t, int i) __attribute__((always_inline)) { load(t, wave + WAVES * i); }, multiply);
   if (whole * STEP < K && wave == whole % WAVES) { // the partial step, zeros past K
     const int k0 = whole * STEP;
     Slot t;

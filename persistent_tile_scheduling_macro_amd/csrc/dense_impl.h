@@ -18,11 +18,11 @@ kernel_fn pick_form(int body) {
       case kFew8: return few_kernel<DT, NK, GATED, 8, BLK, 8>;
       case kFew16: return few_kernel<DT, NK, GATED, 16, BLK, 8>;
       case kFew32: return few_kernel<DT, NK, GATED, 32, BLK, 8>;
-      case kTile64: return tile_kernel<DT, FORM, GATED, 64, 4>;
+      case kTile64: return tile_kernel<DT, FORM, GATED, 64, 6>;
     }
   }
   return body == kPing ? ping_kernel<DT, FORM, GATED> : body == kTile128Pair ? tile_kernel<DT, FORM, GATED, 128, 2>
-                                                                            : tile_kernel<DT, FORM, GATED, 128, 4>;
+                                                                            : tile_kernel<DT, FORM, GATED, 128, 5>;
 }
 template <int DT>
 kernel_fn pick(int body, int form, bool gated) {

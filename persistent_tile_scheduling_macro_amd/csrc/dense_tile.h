@@ -5,13 +5,15 @@
 // wave reads from LDS for the same MFMAs: a 128 x 128 step then costs 64 KiB
 // of LDS reads, 512 clocks, as long as its MFMAs, where eight waves with
 // tiles of 64 x 32 would read 96 KiB. The two halves' sums meet once, in LDS,
-// after the loop, each wave finishing half of the rows.
+// after the loop.
 //
 // The ring: S - 1 steps are in flight. A step waits for its own wave's copies
-// of that stage, passes one barrier (which publishes everyone's copies and
-// tells that the stage read a step ago is free), issues the copies into that
-// stage, reads its fragments and multiplies. Copies past the end of the sum
-// are issued masked, so that every wait counts the same number of loads.
+// of the next stage, passes one barrier (which publishes everyone's copies and
+// tells that the stage multiplied a step ago is free), issues the copies into
+// that stage, and multiplies while it reads the next step's fragments into a
+// second set of registers. With two stages (two workgroups to a CU, whose
+// phases overlap instead) there is one set. Copies past the end of the sum are
+// issued masked, so that every wait counts the same number of loads.
 #pragma once
 
 #include "dense.h"
@@ -26,6 +28,18 @@ using fast::read_b;
 using fast::static_for;
 using fast::wait_vmcnt;
 
+// load16_to_lds as an instruction of its own: of the builtin the compiler knows that it writes LDS, but not which stage,
+// and it waits ahead of a stage's reads for copies in flight into another, which leaves one step in flight (a 128 x 128
+// step then takes 0.55 us instead of 0.4). The kernel's own waits cover every copy; M0 holds the wave's LDS address.
+__device__ inline void copy16(intx4_t rsrc, uint32_t lds, uint32_t voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset), "s"(rsrc)
+               : "memory", "m0");
+}
+__device__ inline intx4_t rsrc_words(const void* base) { // make_rsrc's four words
+  const uint64_t p = (uint64_t)base;
+  return intx4_t{(int)(uint32_t)p, (int)((uint32_t)(p >> 32) & 0xFFFFu), 0x7FFFFFFF, kRsrcWord3};
+}
+
 template <int DT, int FORM, bool GATED, int BM, int S>
 __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
   constexpr int BN = 128, BK = 64;
@@ -35,22 +49,10 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
   constexpr int AL = BM / 64, L = AL + 2; // copies of a wave: of A, and in all
   constexpr int ROW_OC = 256;
   typedef typename fast::Frag<DT>::t frag_t;
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sA1[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sA2[S > 2 ? BM * 128 : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sA3[S > 3 ? BM * 128 : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB1[BN * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB2[S > 2 ? BN * 128 : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB3[S > 3 ? BN * 128 : 16];
-  auto stage_a = [&](auto c) __attribute__((always_inline)) -> uint8_t* {
-    constexpr int C = decltype(c)::value;
-    return C == 0 ? sA0 : C == 1 ? sA1 : C == 2 ? sA2 : sA3;
-  };
-  auto stage_b = [&](auto c) __attribute__((always_inline)) -> uint8_t* {
-    constexpr int C = decltype(c)::value;
-    return C == 0 ? sB0 : C == 1 ? sB1 : C == 2 ? sB2 : sB3;
-  };
+  constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128; // A's tile, then B's
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
+  auto stage_a = [&](auto c) __attribute__((always_inline)) -> uint8_t* { return ring + decltype(c)::value * STAGE; };
+  auto stage_b = [&](auto c) __attribute__((always_inline)) -> uint8_t* { return stage_a(c) + A_BYTES; };
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -83,34 +85,33 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
   };
   const uint16_t* const A = A_KC ? a.a + m0 * a.lda : a.a + m0;
   const uint16_t* const B = (B_KC ? a.b + n0 * a.ldb : a.b + n0) + (GATED && B_KC ? b_up * a.half : 0);
-  auto copy = [&](int step, auto stage) __attribute__((always_inline)) {
-    const int k0 = (first + step) * BK;
-    const int krem = step < nk ? K - k0 : 0;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(A + (A_KC ? (int64_t)k0 : k0 * a.lda));
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (B_KC ? (int64_t)k0 : k0 * a.ldb));
-    uint8_t *pa = stage_a(stage) + 1024 * wave, *pb = stage_b(stage) + 1024 * wave;
-    static_for<AL>([&](auto jc) __attribute__((always_inline)) {
-      constexpr int J = decltype(jc)::value;
+  auto copy_one = [&](int step, auto stage, auto which) __attribute__((always_inline)) { // the wave's copy `which` of a step
+    constexpr int J = decltype(which)::value;
+    const int k0 = (first + step) * BK, krem = step < nk ? K - k0 : 0;
+    const uint32_t to = (uint32_t)(uintptr_t)PGEMM_LDS(uint8_t, stage_a(stage)) + 1024 * wave;
+    uint32_t at;
+    bool ok;
+    if constexpr (J < AL) {
       const int r = a_row + (A_KC ? 64 : 32) * J;
-      const bool ok = A_KC ? (r < mrem) & (8 * a_chunk < krem) : (r < krem) & (8 * a_chunk < mrem);
-      const uint32_t at = (uint32_t)r * (uint32_t)(a.lda * 2) + 16u * (uint32_t)a_chunk;
-      load16_to_lds(ra, pa + 8192 * J, ok ? at : kOOB);
-    });
-    static_for<2>([&](auto jc) __attribute__((always_inline)) {
-      constexpr int J = decltype(jc)::value;
-      uint32_t at;
-      bool ok;
+      ok = A_KC ? (r < mrem) & (8 * a_chunk < krem) : (r < krem) & (8 * a_chunk < mrem);
+      at = (uint32_t)r * (uint32_t)(a.lda * 2) + 16u * (uint32_t)a_chunk;
+      copy16(rsrc_words(A + (A_KC ? (int64_t)k0 : k0 * a.lda)), to + 8192 * J, ok ? at : kOOB);
+    } else {
+      constexpr int JB = J - AL;
       if constexpr (B_KC) {
-        const int r = b_col(J);
+        const int r = b_col(JB);
         ok = (r < nrem) & (8 * b_chunk < krem);
         at = (uint32_t)r * (uint32_t)(a.ldb * 2) + 16u * (uint32_t)b_chunk;
       } else {
-        const int r = b_row + 32 * J, n = b_col(0);
+        const int r = b_row + 32 * JB, n = b_col(0);
         ok = (r < krem) & (n < nrem);
         at = (uint32_t)r * (uint32_t)(a.ldb * 2) + 2u * (uint32_t)n + (GATED ? 2u * (uint32_t)a.half * (uint32_t)b_up : 0u);
       }
-      load16_to_lds(rb, pb + 8192 * J, ok ? at : kOOB);
-    });
+      copy16(rsrc_words(B + (B_KC ? (int64_t)k0 : k0 * a.ldb)), to + A_BYTES + 8192 * JB, ok ? at : kOOB);
+    }
+  };
+  auto copy = [&](int step, auto stage) __attribute__((always_inline)) {
+    static_for<L>([&](auto j) __attribute__((always_inline)) { copy_one(step, stage, j); });
   };
 
   // ---- fragments: the column order of grouped.h, which leaves a lane eight consecutive columns
@@ -137,106 +138,131 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
+  struct Frags { frag_t a[MB], b[4]; };
+  auto read_one_a = [&](Frags& f, auto stage, auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    if constexpr (A_KC) f.a[i] = read_a<DT>(stage_a(stage) + a_off[i], nullptr);
+    else f.a[i] = read_b<DT, ROW_OC>(stage_a(stage) + a_off[i]);
+  };
+  auto read_all_b = [&](Frags& f, auto stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (B_KC) f.b[j] = read_a<DT>(stage_b(stage) + b_off[j], nullptr);
+      else f.b[j] = read_b<DT, ROW_OC>(stage_b(stage) + b_off[j]);
+    }
+  };
+  auto read = [&](Frags& f, auto stage) __attribute__((always_inline)) {
+    read_all_b(f, stage);
+    static_for<MB>([&](auto i) __attribute__((always_inline)) { read_one_a(f, stage, i); });
+  };
+  auto multiply_row = [&](const Frags& f, auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = mfma(f.b[j], f.a[i], acc[i][j]);
+  };
   static_for<S - 1>([&](auto c) __attribute__((always_inline)) { copy(decltype(c)::value, c); });
-  for (int s = 0; s < nk; s += S) {
-    static_for<S>([&](auto c) __attribute__((always_inline)) {
-      constexpr int C = decltype(c)::value;
-      if (s + C < nk) {
-        wait_vmcnt<(S - 2) * L>();
-        pp::barrier_raw();
-        copy(s + C + S - 1, std::integral_constant<int, (C + S - 1) % S>{});
-        const uint8_t *pa = stage_a(c), *pb = stage_b(c);
-        frag_t af[MB], bf[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (B_KC) bf[j] = read_a<DT>(pb + b_off[j], nullptr);
-          else bf[j] = read_b<DT, ROW_OC>(pb + b_off[j]);
+  if constexpr (S == 2) {
+    for (int s = 0; s < nk; s += 2) {
+      static_for<2>([&](auto c) __attribute__((always_inline)) {
+        constexpr int C = decltype(c)::value;
+        if (s + C < nk) {
+          wait_vmcnt<0>();
+          pp::barrier_raw();
+          copy(s + C + 1, std::integral_constant<int, C ^ 1>{});
+          Frags f;
+          read(f, c);
+          static_for<MB>([&](auto i) __attribute__((always_inline)) { multiply_row(f, i); });
         }
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          if constexpr (A_KC) af[i] = read_a<DT>(pa + a_off[i], nullptr);
-          else af[i] = read_b<DT, ROW_OC>(pa + a_off[i]);
+      });
+    }
+  } else {
+    constexpr int U = S % 2 ? 2 * S : S; // steps after which stages and register sets repeat
+    Frags f[2];
+    wait_vmcnt<(S - 2) * L>();
+    pp::barrier_raw();
+    read(f[0], std::integral_constant<int, 0>{});
+    for (int s = 0; s < nk; s += U) {
+      static_for<U>([&](auto c) __attribute__((always_inline)) {
+        constexpr int C = decltype(c)::value;
+        if (s + C < nk) {
+          wait_vmcnt<(S - 3) * L>(); // the next step's copies
+          pp::barrier_raw();
+          // between the rows' MFMAs: the copies into the freed stage, the next step's fragments
+          std::integral_constant<int, (C + S - 1) % S> freed;
+          std::integral_constant<int, (C + 1) % S> next;
+          static_for<MB>([&](auto i) __attribute__((always_inline)) {
+            constexpr int I = decltype(i)::value;
+            multiply_row(f[C % 2], i);
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<L * (I + 1) / MB - L * I / MB>([&](auto j) __attribute__((always_inline)) {
+              copy_one(s + C + S - 1, freed, std::integral_constant<int, L * I / MB + decltype(j)::value>{});
+            });
+            if constexpr (I == 0) read_all_b(f[(C + 1) % 2], next);
+            read_one_a(f[(C + 1) % 2], next, i);
+            __builtin_amdgcn_sched_barrier(0);
+          });
         }
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = mfma(bf[j], af[i], acc[i][j]);
-      }
-    });
+      });
+    }
   }
 
-  // ---- the two halves of the steps: each wave gives the rows it does not finish
+  // ---- output. Both halves of the steps go to LDS as fp32 rows (in two turns where LDS holds half of them) and come
+  // back added, eight columns a thread and 16 threads (gated: 8) to a row, so that a row's stores are 256 bytes side by
+  // side: from the MFMA's layout they would be 64, which at the odd addresses of odd N takes three times as long. The
+  // 16-byte chunk c of row r lies at c ^ (r & 15).
   wait_vmcnt<0>(); // the masked copies write LDS too
-  __syncthreads();
-  constexpr int HB = MB / 2;
-  {
-    uint8_t* part = (wave & 2 ? (wave & 1 ? sB1 : sB0) : (wave & 1 ? sA1 : sA0)) + (BM * 64) * kw; // HB * 4 KiB a wave
-    floatx4_t* to = reinterpret_cast<floatx4_t*>(part);
-#pragma unroll
-    for (int i = 0; i < HB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) to[(i * 4 + j) * 64 + lane] = kw ? acc[i][j] : acc[HB + i][j];
-  }
-  __syncthreads();
-  {
-    const uint8_t* part = (wave & 2 ? (wave & 1 ? sB1 : sB0) : (wave & 1 ? sA1 : sA0)) + (BM * 64) * (kw ^ 1);
-    const floatx4_t* from = reinterpret_cast<const floatx4_t*>(part);
-#pragma unroll
-    for (int i = 0; i < HB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const floatx4_t o = from[(i * 4 + j) * 64 + lane], mine = kw ? acc[HB + i][j] : acc[i][j];
-        acc[i][j] = kw ? o + mine : mine + o; // the first half's sum first
-      }
-  }
-
-  // ---- output
-  const bool odd = (g & 1) != 0;
+  constexpr int TURNS = 2 * BM * 512 > S * STAGE ? 2 : 1, ROWS = BM / TURNS, HB = MB / TURNS; // rows of a turn
+  static_assert(2 * ROWS * 512 <= S * STAGE && MB % TURNS == 0, "both halves of a turn's rows fit the stages");
   const Epilogue<DT, GATED> epilogue(a);
-  auto row_of = [&](int i) __attribute__((always_inline)) {
-    const int b = kw * HB + i;
-    return m0 + wm * (BM / 2) + (A_KC ? 16 * b + s16 : 32 * (b >> 1) + 8 * q + 4 * ((b + q) & 1) + qt);
+  constexpr int LANES = GATED ? 8 : 16; // to a row
+  const int c8 = tid % LANES, n = n0 + 8 * c8;
+  const int col = GATED ? (c8 >> 2) * 64 + 8 * (c8 & 3) : 8 * c8; // tile column of the thread's first; up: 32 further
+  float bv[8], bu[8];
+  if (a.split <= 1) epilogue.bias_of(n, bv, bu);
+  auto at = [&](int half, int r, int chunk) __attribute__((always_inline)) -> floatx4_t* { // stages follow each other in `ring`
+    return reinterpret_cast<floatx4_t*>(ring + half * (ROWS * 512) + r * 512 + 16 * (chunk ^ (r & 15)));
   };
-  auto eight = [&](int i, int P, float* v) __attribute__((always_inline)) {
+  // A turn's rows: of each wave row wm its blocks turn * HB .. + HB - 1
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      v[r] = odd ? acc[i][2 * P + 1][r] : acc[i][2 * P][r];
-      v[4 + r] = odd ? acc[i][2 * P][r] : acc[i][2 * P + 1][r];
-    }
-  };
-  if (a.split > 1) {
-    const int64_t ld = part_ld(a, GATED);
-#pragma unroll
-    for (int P = 0; P < 2; ++P) {
-      const int n = n0 + (GATED ? wn * 32 : wn * 64 + 32 * P) + 8 * g;
-      if (n >= a.N) continue;
-      float* col = a.part + (int64_t)piece * a.M * ld + n + (GATED && P ? ld / 2 : 0);
-#pragma unroll
-      for (int i = 0; i < HB; ++i) {
-        const int m = row_of(i);
-        float v[8];
-        eight(i, P, v);
-        if (m < a.M) {
-          float* to = col + m * ld;
-          *reinterpret_cast<floatx4_t*>(to) = floatx4_t{v[0], v[1], v[2], v[3]};
-          *reinterpret_cast<floatx4_t*>(to + 4) = floatx4_t{v[4], v[5], v[6], v[7]};
-        }
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int P = 0; P < (GATED ? 1 : 2); ++P) {
-    const int n = n0 + (GATED ? wn * 32 : wn * 64 + 32 * P) + 8 * g;
-    float bv[8], bu[8];
-    epilogue.bias_of(n, bv, bu);
+  for (int turn = 0; turn < TURNS; ++turn) {
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < HB; ++i) {
-      const int m = row_of(i);
+      const int r = wm * (16 * HB) + (A_KC ? 16 * i + s16 : 32 * (i >> 1) + 8 * q + 4 * ((i + q) & 1) + qt);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) // columns 64 wn + 32 (j / 2) + 8 g + 4 ((j + g) & 1) ..
+        *at(kw, r, 16 * wn + 8 * (j >> 1) + 2 * g + ((j + g) & 1)) = acc[turn * HB + i][j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < ROWS * LANES / 512; ++pass) {
+      const int r = tid / LANES + pass * (512 / LANES);
+      const int m = m0 + (r / (16 * HB)) * (BM / 2) + turn * (16 * HB) + r % (16 * HB);
       float v[8], w[8];
-      eight(i, P, v);
-      if constexpr (GATED) eight(i, 1, w);
-      if (m < a.M && n < a.N) epilogue.finish(m, n, v, w, bv, bu);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const floatx4_t x = *at(0, r, col / 4 + h) + *at(1, r, col / 4 + h);
+        floatx4_t y = x;
+        if constexpr (GATED) y = *at(0, r, col / 4 + 8 + h) + *at(1, r, col / 4 + 8 + h);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[4 * h + k] = x[k];
+          w[4 * h + k] = y[k];
+        }
+      }
+      if (m >= a.M || n >= a.N) continue;
+      if (a.split > 1) {
+        const int64_t ld = part_ld(a, GATED);
+        float* to = a.part + ((int64_t)piece * a.M + m) * ld + n;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<floatx4_t*>(to + 4 * h) = floatx4_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+          if constexpr (GATED)
+            *reinterpret_cast<floatx4_t*>(to + ld / 2 + 4 * h) = floatx4_t{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+        }
+      } else {
+        epilogue.finish(m, n, v, w, bv, bu);
+      }
     }
   }
 }

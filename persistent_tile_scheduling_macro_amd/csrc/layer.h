@@ -47,6 +47,7 @@ struct Args {
   float* shares;         // [awake][kTokens]
   uint16_t* out;         // [T, H]
   int T, k, E, H, I, act;
+  int most; // experts that can be awake
 };
 
 __device__ inline void wave_fence() { // LDS serves a wave in order: only the compiler has to be held
@@ -57,7 +58,7 @@ __device__ inline void wave_fence() { // LDS serves a wave in order: only the co
 // MB: blocks of 16 rows that T tokens can need.
 template <int DT, bool GATED, int MB>
 __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
-  constexpr int WAVES = 8, BLK = GATED ? 2 : 1, D = 2, XL = 2 * MB;
+  constexpr int WAVES = 8, BLK = GATED ? 2 : 1, D = MB > 1 ? 2 : GATED ? 3 : 4, XL = 2 * MB;
   constexpr int TURN = 2048 * (MB + BLK), JOIN = BLK * MB * 1024;
   typedef typename fast::Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;
@@ -98,7 +99,9 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
   for (; skip > 0; --skip) bits &= bits - 1;
   const int e = 32 * at + __builtin_ctz(bits);
 
-  // every wave finds the rows for itself: lane t looks through its token's choices
+  // every wave finds the rows for itself: lane t looks through its token's choices, and the tokens that
+  // have one move to the front
+  const int n0 = blockIdx.x * 16, row = lane >> 3, chunk = lane & 7;
   int slot = -1;
   float share = 0.0f;
   if (lane < a.T) {
@@ -108,25 +111,24 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
       for (int j = 0; j < a.k; ++j)
         if (s_ids[lane * a.k + j] == e) share += a.weights[lane * a.k + j];
   }
-  const uint64_t taken = __ballot(slot >= 0);
+  const uint64_t taken = __ballot(slot >= 0), below = (1ull << lane) - 1;
   const int rows = (int)__popcll(taken);
+  const int rank = slot >= 0 ? (int)__popcll(taken & below) : rows + (int)__popcll(~taken & below);
+  const int slot_at = __builtin_amdgcn_ds_permute(4 * rank, slot); // lane r: the slot of row r
   if (wave == 0 && slot >= 0) {
-    const int r = (int)__popcll(taken & ((1ull << lane) - 1));
-    s_row[r] = slot;
+    s_row[rank] = slot; // read after the next barrier
     if (writes) {
-      a.slots[which * kTokens + r] = slot;
-      a.shares[which * kTokens + r] = share;
+      a.slots[which * kTokens + rank] = slot;
+      a.shares[which * kTokens + rank] = share;
     }
   }
   if (writes && tid == 0) a.awake[1 + which] = e | rows << 16;
-  __syncthreads();
 
   // ---- the product
-  const int n0 = blockIdx.x * 16, row = lane >> 3, chunk = lane & 7;
   const int x_loads = __builtin_amdgcn_readfirstlane((rows + 7) >> 3), blocks = (x_loads + 1) >> 1;
   const uint16_t* x[XL];
 #pragma unroll
-  for (int i = 0; i < XL; ++i) x[i] = a.x + s_row[min(8 * i + row, rows - 1)] / a.k * a.ldx + 8 * chunk;
+  for (int i = 0; i < XL; ++i) x[i] = a.x + __shfl(slot_at, min(8 * i + row, rows - 1)) / a.k * a.ldx + 8 * chunk;
   const uint16_t* w[BLK * 2];
 #pragma unroll
   for (int i = 0; i < BLK * 2; ++i)
@@ -171,19 +173,8 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
     }
   };
   const int whole = H / 64, mine = (whole - wave + WAVES - 1) / WAVES;
-  if (mine > 0) {
-    auto step_of = [&](int i) __attribute__((always_inline)) { return wave + WAVES * min(i, mine - 1); };
-    Slot t[D];
-#pragma unroll
-    for (int j = 0; j < D; ++j) load(t[j], step_of(j));
-    for (int i = 0; i < mine; i += D) {
-#pragma unroll
-      for (int j = 0; j < D; ++j) {
-        if (i + j < mine) multiply(t[j]);
-        load(t[j], step_of(i + j + D)); // past the range the last one again, not used
-      }
-    }
-  }
+  dense::stream_steps<D, Slot>(
+      mine, [&](Slot& t, int i) __attribute__((always_inline)) { load(t, wave + WAVES * i); }, multiply);
   if (whole * 64 < H && wave == whole % WAVES) { // the partial step, zeros past H
     const int k0 = whole * 64;
     Slot t;
@@ -225,9 +216,13 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
   }
 }
 
+// Waves of a workgroup of down_kernel: there are only H / 16 workgroups, so as many as LDS holds (16 columns of 2048 rows
+// and eight experts of I = 1024: 17 us with eight waves, 12.5 us with 16).
+constexpr int down_waves(int blocks) { return blocks == 4 ? 8 : 16; }
+
 template <int DT, int MB>
-__global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
-  constexpr int WAVES = 8, D = MB == 1 ? 4 : 2, XL = 2 * MB, RING = 8;
+__global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_kernel(Args a) {
+  constexpr int WAVES = down_waves(MB), D = MB == 1 ? 4 : 2, XL = 2 * MB, RING = MB == 1 ? 8 : 4;
   static_assert(D < RING, "a ring entry lasts from an expert's first load to its last product");
   constexpr int TURN = 2048 * (MB + 1), TOKENS = 16 * MB;
   typedef typename fast::Frag<DT>::t frag_t;
@@ -241,63 +236,62 @@ __global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, s = lane & 15, row = lane >> 3, chunk = lane & 7;
   const int n0 = blockIdx.x * 16, H = a.H, I = a.I;
-  const int awake = __builtin_amdgcn_readfirstlane(a.awake[0]);
+  const int infos = a.awake[min(lane, a.most)]; // lane 0: how many; then the first experts
+  for (int i = lane; i < TOKENS * 4; i += 64) s_out[wave][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  const int awake = __builtin_amdgcn_readfirstlane(infos);
   const int steps = (I + 63) / 64;
   const int64_t units = (int64_t)awake * steps;
   const int64_t from = units * wave / WAVES, to = units * (wave + 1) / WAVES;
-  for (int i = lane; i < TOKENS * 4; i += 64) s_out[wave][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  const int mine = (int)(to - from);
 
-  // ---- the load cursor: expert, step, its rows' slots in the lanes, and the next expert's
-  int l_at = (int)(from / steps), l_step = (int)(from - (int64_t)l_at * steps);
-  int64_t left = to - from;
-  int next_info = 0, next_slot = 0;
+  // ---- the load cursor: expert, step, the slots and shares of its rows in the lanes (fetched an expert ahead)
+  int l_at = (int)(from / steps), l_step = (int)(from - (int64_t)l_at * steps), l_loads = 0;
+  bool fresh = true; // expert l_at has not been entered
+  int next_slot = 0;
   float next_share = 0.0f;
-  auto fetch = [&](int at) __attribute__((always_inline)) {
-    const int i = min(at, awake - 1);
-    next_info = a.awake[1 + i];
-    next_slot = a.slots[i * kTokens + lane]; // lanes past the rows hold whatever is there
-    next_share = a.shares[i * kTokens + lane];
+  auto fetch = [&](int at) __attribute__((always_inline)) { // lanes past the rows read what nobody uses
+    const int i = min(at, awake - 1) * kTokens + lane;
+    next_slot = a.slots[i];
+    next_share = a.shares[i];
   };
   const uint16_t* w[2];
-  int x[XL], l_loads = 0; // element offsets in h
-  auto enter = [&]() __attribute__((always_inline)) { // expert l_at's rows come into use
-    const int info = __builtin_amdgcn_readfirstlane(next_info), e = info & 0xFFFF, rows = info >> 16;
-    const int slot = next_slot;
-    const float share = next_share;
-    if (lane < TOKENS) {
-      s_token[wave][l_at % RING][lane] = lane < rows ? slot / a.k : -1;
-      s_share[wave][l_at % RING][lane] = share;
-    }
-    l_loads = (rows + 7) >> 3;
-#pragma unroll
-    for (int i = 0; i < XL; ++i) x[i] = __shfl(slot, min(8 * i + row, rows - 1)) * I + 8 * chunk;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = a.w_out + ((int64_t)e * H + min(n0 + 8 * i + row, H - 1)) * I + 8 * chunk;
-    fetch(l_at + 1);
-  };
-  struct Slot { u32x4 x[XL], w[2]; };
+  int x[XL], l_rows = 0; // element offsets in h
+  struct Slot { u32x4 x[XL], w[2]; int loads; };
+  int left = mine;
   auto load = [&](Slot& t) __attribute__((always_inline)) {
     if (left <= 0) return;
     --left;
-    const int k0 = l_step * 64;
-    if (k0 + 64 <= I) {
+    if (fresh) {
+      const int info = __builtin_amdgcn_readfirstlane(l_at < 63 ? __shfl(infos, l_at + 1) : a.awake[1 + l_at]);
+      l_rows = info >> 16;
+      l_loads = (l_rows + 7) >> 3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
-#pragma unroll
-      for (int i = 0; i < XL; ++i)
-        if (i < l_loads) t.x[i] = moe::load8<moe::kAnyAddress>(a.h + x[i] + k0);
-    } else {
-      const int rest = I - k0 - 8 * chunk;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) t.w[i] = load_upto(w[i] + k0, rest, I);
-#pragma unroll
-      for (int i = 0; i < XL; ++i)
-        if (i < l_loads) t.x[i] = load_upto(a.h + x[i] + k0, rest, I);
+      for (int i = 0; i < 2; ++i) w[i] = a.w_out + ((int64_t)(info & 0xFFFF) * H + min(n0 + 8 * i + row, H - 1)) * I + 8 * chunk;
     }
+    const int k0 = l_step * 64, rest = I - k0 - 8 * chunk;
+    const bool part = k0 + 64 > I;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) t.w[i] = part ? load_upto(w[i] + k0, rest, I) : moe::load8<moe::kAnyAddress>(w[i] + k0);
+    if (fresh) { // the slots come in while the matrix is read
+      const int slot = next_slot;
+      const float share = next_share;
+      if (lane < TOKENS) {
+        s_token[wave][l_at % RING][lane] = lane < l_rows ? slot / a.k : -1;
+        s_share[wave][l_at % RING][lane] = share;
+      }
+#pragma unroll
+      for (int i = 0; i < XL; ++i) x[i] = __shfl(slot, min(8 * i + row, l_rows - 1)) * I + 8 * chunk;
+      fetch(l_at + 1);
+      fresh = false;
+    }
+    t.loads = l_loads;
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if (i < l_loads) t.x[i] = part ? load_upto(a.h + x[i] + k0, rest, I) : moe::load8<moe::kAnyAddress>(a.h + x[i] + k0);
     if (++l_step == steps) {
       l_step = 0;
       ++l_at;
-      if (left > 0) enter();
+      fresh = true;
     }
   };
 
@@ -307,6 +301,7 @@ __global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b] = floatx4_t{0.f, 0.f, 0.f, 0.f};
   auto flush = [&]() __attribute__((always_inline)) { // expert c_at's sums to their tokens
+    wave_fence();
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       const int token = s_token[wave][c_at % RING][16 * b + s];
@@ -325,7 +320,8 @@ __global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
   auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
     wave_fence(); // the last step's reads come first
 #pragma unroll
-    for (int i = 0; i < XL; ++i) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
+    for (int i = 0; i < XL; ++i)
+      if (i < t.loads) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
 #pragma unroll
     for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
     wave_fence();
@@ -334,26 +330,23 @@ __global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
       const frag_t f = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(s, 4 * h + g));
 #pragma unroll
       for (int b = 0; b < MB; ++b)
-        acc[b] = mfma(f, *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(16 * b + s, 4 * h + g)), acc[b]);
+        if (2 * b < t.loads) {
+          // an odd number of loads leaves the block's upper half to repeat its lower one
+          const int r = 16 * b + (2 * b + 1 < t.loads ? s : s & 7);
+          acc[b] = mfma(f, *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(r, 4 * h + g)), acc[b]);
+        }
     }
     if (++c_step == steps) {
-      wave_fence();
       flush();
       c_step = 0;
       ++c_at;
     }
   };
-  const int mine = (int)(to - from);
   if (mine > 0) {
     fetch(l_at);
-    enter();
     Slot t[D];
 #pragma unroll
-    for (int j = 0; j < D; ++j) {
-#pragma unroll
-      for (int i = 0; i < XL; ++i) t[j].x[i] = u32x4{0, 0, 0, 0}; // rows that no load fills
-      load(t[j]);
-    }
+    for (int j = 0; j < D; ++j) load(t[j]);
     for (int i = 0; i < mine; i += D) {
 #pragma unroll
       for (int j = 0; j < D; ++j)
@@ -362,10 +355,7 @@ __global__ void __launch_bounds__(512, MB == 4 ? 2 : 4) down_kernel(Args a) {
           load(t[j]);
         }
     }
-    if (c_step) {
-      wave_fence();
-      flush(); // the next wave has the rest of this expert's sum
-    }
+    if (c_step) flush(); // the next wave has the rest of this expert's sum
   }
   __syncthreads();
   const float* parts = reinterpret_cast<const float*>(s_out);

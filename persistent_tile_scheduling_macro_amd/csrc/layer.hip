@@ -88,11 +88,11 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
     a.weights = weights + t * k;
     a.out = static_cast<uint16_t*>(out) + t * H;
     const int blocks = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-    const int64_t n = a.T * k;
-    e = enqueue(h->stream, dim3((unsigned)((I + 15) / 16), (unsigned)(E < n ? E : n)), dim3(512),
+    a.most = (int)(E < a.T * k ? E : a.T * k);
+    e = enqueue(h->stream, dim3((unsigned)((I + 15) / 16), (unsigned)a.most), dim3(512),
                 f16 ? layer::up_f16(gated, blocks) : layer::up_bf16(gated, blocks), a);
     if (e == hipSuccess)
-      e = enqueue(h->stream, dim3((unsigned)((H + 15) / 16)), dim3(512), f16 ? layer::down_f16(blocks) : layer::down_bf16(blocks), a);
+      e = enqueue(h->stream, dim3((unsigned)((H + 15) / 16)), dim3(64 * layer::down_waves(blocks)), f16 ? layer::down_f16(blocks) : layer::down_bf16(blocks), a);
   }
   return launch_status(h, e, "routed layer");
 }
