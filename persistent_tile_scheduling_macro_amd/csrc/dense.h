@@ -53,12 +53,22 @@ __device__ inline u32x4 load8_upto(const uint16_t* row, int64_t n, int64_t N) {
 }
 
 // What follows the sums of eight columns n .. n+7 of row m (n < N): v the sums
-// (gated: of the gate), u those of up.
-template <int DT, bool GATED>
+// (gated: of the gate), u those of up. The activation's path is chosen around
+// the loops over a tile's rows (act::with_path), so that what runs lies together.
+// EVEN: N is a multiple of 8.
+template <int DT, bool GATED, bool EVEN = false>
 struct Epilogue {
   const Args& a;
   const act::Consts k;
   __device__ explicit Epilogue(const Args& a_) : a(a_), k(act::consts_of(a_.act)) {}
+
+  __device__ inline u32x4 load(const uint16_t* row, int n) const {
+    return EVEN ? moe::load8<moe::kAnyAddress>(row + n) : load8_upto(row, n, a.N);
+  }
+  __device__ inline void store(uint16_t* row, int n, const float* v) const {
+    if constexpr (EVEN) moe::store8<moe::kAnyAddress>(row + n, moe::pack<DT>(v));
+    else moe::store_row<moe::kAnyAddress>(row, n, a.N, moe::pack<DT>(v));
+  }
 
   __device__ inline void bias_of(int n, float* bv, float* bu) const {
 #pragma unroll
@@ -68,10 +78,11 @@ struct Epilogue {
       for (int i = 0; i < 8; ++i) bu[i] = 0.0f;
     }
     if (!a.bias || n >= a.N) return;
-    moe::unpack<DT>(load8_upto(a.bias, n, a.N), bv);
-    if constexpr (GATED) moe::unpack<DT>(load8_upto(a.bias + a.N, n, a.N), bu);
+    moe::unpack<DT>(load(a.bias, n), bv);
+    if constexpr (GATED) moe::unpack<DT>(load(a.bias + a.N, n), bu);
   }
 
+  template <int PATH>
   __device__ inline void finish(int m, int n, float* v, float* u, const float* bv, const float* bu) const {
     const int64_t N = a.N;
 #pragma unroll
@@ -81,18 +92,16 @@ struct Epilogue {
     }
     if (a.z) {
       uint16_t* z = a.z + (int64_t)m * (GATED ? 2 * N : N);
-      moe::store_row<moe::kAnyAddress>(z, n, (int)N, moe::pack<DT>(v));
-      if constexpr (GATED) moe::store_row<moe::kAnyAddress>(z + N, n, (int)N, moe::pack<DT>(u));
+      store(z, n, v);
+      if constexpr (GATED) store(z + N, n, u);
     }
     u32x4 res = {0, 0, 0, 0};
     if (a.residual) res = load8_upto(a.residual + m * a.ldr, n, N);
-    act::with_path(k, [&](auto path) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = act::value<decltype(path)::value>(v[i], k);
-        if constexpr (GATED) v[i] *= u[i];
-      }
-    });
+    for (int i = 0; i < 8; ++i) {
+      v[i] = act::value<PATH>(v[i], k);
+      if constexpr (GATED) v[i] *= u[i];
+    }
     if (a.residual) {
       float r[8];
       moe::unpack<DT>(res, r);
@@ -123,6 +132,18 @@ template <int D, class Slot, class L, class F>
 __device__ inline void stream_steps(int n, L load, F multiply) {
   if (n >= D) stream_loop<D, Slot>(n, load, multiply);
   else if (n > 0) stream_loop<D < 2 ? D : 2, Slot>(n, load, multiply);
+}
+
+// load16_to_lds as an instruction of its own: of the builtin the compiler knows that it writes LDS, but not which stage,
+// and it waits ahead of a stage's reads for copies in flight into another, which leaves one step in flight (a 128 x 128
+// step then takes 0.55 us instead of 0.4). The kernel's own waits cover every copy; M0 holds the wave's LDS address.
+__device__ inline void copy16(intx4_t rsrc, uint32_t lds, uint32_t voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset), "s"(rsrc)
+               : "memory", "m0");
+}
+__device__ inline intx4_t rsrc_words(const void* base) { // make_rsrc's four words
+  const uint64_t p = (uint64_t)base;
+  return intx4_t{(int)(uint32_t)p, (int)((uint32_t)(p >> 32) & 0xFFFFu), 0x7FFFFFFF, kRsrcWord3};
 }
 
 // The step range of piece `piece`: first step and steps of 64.

@@ -11,7 +11,6 @@ using dense::Args;
 constexpr int64_t kMaxSize = (int64_t)1 << 30;
 // Row strides up to which a tile's 32-bit offsets reach its last row (256 rows of 2-byte elements below 2^31).
 constexpr int64_t kMaxDirectStride = (int64_t)1 << 21;
-constexpr int kFewRows = 32; // up to so many, one pass over W
 
 // One chunk of eight a thread.
 __global__ void __launch_bounds__(256) pad_rows_kernel(dense::PadArgs p) {
@@ -50,30 +49,94 @@ struct Plan { int body; int split; };
 struct Tile { int bm, bn; };
 Tile tile_of(int body) { return body == dense::kPing ? Tile{256, 256} : body == dense::kTile64 ? Tile{64, 128} : Tile{128, 128}; }
 
-// Body and pieces of a product of M x K with K x C (C columns before gating).
-Plan plan_rows(int64_t M, int64_t N, int64_t K, int form, bool gated) {
-  if (M <= kFewRows && (form == dense::kRowsNK || N >= 4))
-    return {M <= 8 ? dense::kFew8 : M <= 16 ? dense::kFew16 : dense::kFew32, 1};
+// The bodies' times in us on 256 CUs, fitted to some 2900 measured calls of 1 .. 8192 rows and 64 .. 8192 columns and sums
+// (replayed from a graph, bf16, operands changing from call to call); the rule below was 2% slower than the best of them
+// in the geometric mean, 36% at worst. Examples (the times of few, tile 64, tile 128, pair, ping-pong, each with its
+// best number of pieces): 24 x 4096 x 4096 9, 14, 16, 18, 27; 512 x 4096 x 8192 -, 71, 43, 53, 59; 4099 x 2056 x 1024
+// -, -, 36, 31, 36; 8192 x 8192 x 4096 -, -, 615, 545, 455.
+//
+// few: base + the longer of rounds of 256 workgroups, each `start` and `step` for each k, and reading W for every
+// group of rows at `rate` TB/s.
+struct FewCost { double base, start, step, rate; };
+constexpr FewCost kFewCost[2][2][3] = { // K x N, N x K; plain, gated; 8, 16, 32 rows
+    {{{2.4, 0.4, 0.00315, 6.5}, {3.0, 0.0, 0.00315, 4.0}, {3.3, 0.0, 0.0037, 3.4}},
+     {{3.2, 0.0, 0.0049, 2.8}, {4.9, 0.5, 0.0038, 6.3}, {5.1, 0.0, 0.0045, 3.8}}},
+    {{{1.6, 0.6, 0.00096, 5.4}, {2.1, 0.65, 0.0010, 6.0}, {2.5, 0.45, 0.0010, 5.5}},
+     {{3.4, 0.0, 0.0009, 6.5}, {1.5, 1.1, 0.00175, 6.0}, {1.9, 1.0, 0.0022, 5.3}}}};
+// tiles: base + rounds of workgroups, each `start` and for each 64 k `step`, or `full` when every CU has one (two); at
+// least the operands' bytes at 5 TB/s; pieces cost `join` and `join_sum` for each million partial sums.
+struct TileCost { double base, start, step, full, join, join_sum; };
+constexpr TileCost kTileCost[4] = {{2.5, 1.9, 0.285, 0.51, 1.9, 1.87},  // kTile64
+                                   {2.8, 3.2, 0.38, 0.525, 1.2, 1.86},  // kTile128
+                                   {5.1, 0.0, 0.695, 1.04, 0.7, 2.15},  // kTile128Pair
+                                   {9.9, 0.45, 1.19, 1.63, 0.0, 1.25}}; // kPing
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int few_rows(int body) { return body == dense::kFew8 ? 8 : body == dense::kFew16 ? 16 : 32; }
+int few_columns(bool nk) { return nk ? 16 : 64; } // of y
+
+double few_time(int body, int64_t M, int64_t N, int64_t K, bool nk, bool gated) {
+  const FewCost& c = kFewCost[nk][gated][body - dense::kFew8];
+  const double groups = (double)ceil_div(M, few_rows(body));
+  const double work = (double)ceil_div((int64_t)groups * ceil_div(N, few_columns(nk)), 256) * (c.start + c.step * K);
+  const double reads = groups * K * (gated ? 2 : 1) * N * 2e-6 / c.rate;
+  return c.base + (work > reads ? work : reads);
+}
+double tile_time(int body, int64_t rows, int64_t columns, int64_t sum, int64_t pieces) {
+  const TileCost& c = kTileCost[body - dense::kTile64];
+  const Tile t = tile_of(body);
+  const int64_t groups = ceil_div(rows, t.bm) * ceil_div(columns, t.bn) * pieces;
+  const int64_t slots = body == dense::kTile128Pair ? 512 : 256;
+  double load = groups / 256.0 - (slots == 512);
+  load = load < 0 ? 0 : load > 1 ? 1 : load;
+  const double work = (double)ceil_div(groups, slots) * (c.start + (double)ceil_div(sum, 64) / pieces * (c.step + (c.full - c.step) * load));
+  const double reads = 2.0 * ((double)rows * sum + (double)sum * columns + (double)rows * columns) / 5e6;
+  const double join = pieces > 1 ? c.join + 0.15 * pieces + c.join_sum * 1e-6 * pieces * rows * columns : 0;
+  return c.base + (work > reads ? work : reads) + join;
+}
+
+// Tries a tile body with the numbers of pieces that leave each at least two steps of 64.
+void try_tiles(int body, int64_t rows, int64_t columns, int64_t sum, double extra, Plan* best, double* least) {
+  const int64_t steps = ceil_div(sum, 64);
+  for (int pieces : {1, 2, 3, 4, 6, 8, 12}) {
+    if (pieces > 1 && (pieces * 2 > steps || (body == dense::kTile128Pair && pieces > 4))) break;
+    const Tile t = tile_of(body);
+    if (pieces > 1 && ceil_div(rows, t.bm) * ceil_div(columns, t.bn) * pieces > 1024) break;
+    const double time = extra + tile_time(body, rows, columns, sum, pieces);
+    if (time < *least) *best = {body, pieces}, *least = time;
+  }
+}
+
+// Body and pieces of a product of M x K with K x N (gated: 2N) columns. pad_x, pad_w: sizes whose rows the tile bodies
+// need moved first (a launch of 3 us and a pass over the operand).
+Plan plan_rows(int64_t M, int64_t N, int64_t K, bool nk, bool gated, bool pad_x, bool pad_w) {
   const int64_t C = gated ? 2 * N : N;
-  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((C + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return {dense::kPing, 1};
-  const int body = M <= 64 ? dense::kTile64 : dense::kTile128;
-  const int64_t t = tiles(tile_of(body).bm, 128), steps = (K + 63) / 64;
-  int64_t split = t < 256 ? 256 / t : 1;
-  if (split > steps / 4) split = steps / 4 > 0 ? steps / 4 : 1;
-  if (split > 16) split = 16;
-  return {body, (int)split};
+  Plan best = {dense::kTile128, 1};
+  double least = 1e30;
+  const double extra = pad_x * (3 + 1e-6 * M * K) + pad_w * (3 + 1e-6 * C * K);
+  if (N % 8 == 0) try_tiles(dense::kPing, M, C, K, extra, &best, &least);
+  try_tiles(dense::kTile128, M, C, K, extra, &best, &least);
+  try_tiles(dense::kTile128Pair, M, C, K, extra, &best, &least);
+  if (M <= 512) try_tiles(dense::kTile64, M, C, K, extra, &best, &least);
+  if (M <= 128 && (nk || N >= 4)) {
+    for (int body : {(int)dense::kFew8, (int)dense::kFew16, (int)dense::kFew32}) {
+      if (M > 16 ? body == dense::kFew8 : few_rows(body) / 2 >= M && body > dense::kFew8) continue;
+      const double time = few_time(body, M, N, K, nk, gated);
+      if (time < least) best = {body, 1}, least = time;
+    }
+  }
+  return best;
 }
 
 // The same for c [I][J] = a^T b over R rows.
 Plan plan_grad(int64_t R, int64_t I, int64_t J) {
-  auto tiles = [&](int bm) { return ((I + bm - 1) / bm) * ((J + bm - 1) / bm); };
-  if (tiles(256) >= 192 && R > 256) return {dense::kPing, 1};
-  const int64_t t = tiles(128), steps = (R + 63) / 64;
-  int64_t split = t < 256 && t > 0 ? 256 / t : 1;
-  if (split > steps / 4) split = steps / 4 > 0 ? steps / 4 : 1;
-  if (split > 16) split = 16;
-  return {steps <= 4 && t > 256 ? dense::kTile128Pair : dense::kTile128, (int)split};
+  Plan best = {dense::kTile128, 1};
+  double least = 1e30;
+  if (J % 8 == 0) try_tiles(dense::kPing, I, J, R, 0, &best, &least);
+  try_tiles(dense::kTile128, I, J, R, 0, &best, &least);
+  try_tiles(dense::kTile128Pair, I, J, R, 0, &best, &least);
+  return best;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
@@ -117,8 +180,7 @@ struct Call {
     if (!h) return;
     const dense::kernel_fn kernel = kernels.pick(plan.body, form, gated);
     if (plan.body <= dense::kFew32) {
-      const int rows = plan.body == dense::kFew8 ? 8 : plan.body == dense::kFew16 ? 16 : 32;
-      const int wide = form == dense::kRowsNK ? 16 : 64;
+      const int rows = few_rows(plan.body), wide = few_columns(form == dense::kRowsNK);
       if (status == hipSuccess)
         status = enqueue(h->stream, dim3((unsigned)((a.N + wide - 1) / wide), (unsigned)((a.M + rows - 1) / rows)), dim3(512), kernel, a);
       return;
@@ -153,7 +215,7 @@ int check(pgemm_ctx* h, int64_t M, int64_t N, int64_t K, int layout, int act, in
 int forward(Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, bool wide_x, bool wide_w, Args a, int layout, bool gated) {
   const bool nk = layout == PGEMM_B_NK;
   const int form = nk ? dense::kRowsNK : dense::kRowsKN;
-  const Plan plan = plan_rows(a.M, a.N, a.K, form, gated);
+  const Plan plan = plan_rows(a.M, a.N, a.K, nk, gated, a.K % 8, (nk ? a.K : a.N) % 8);
   const int64_t columns = gated ? 2 * (int64_t)a.N : a.N;
   if (plan.body <= dense::kFew32) {
     a.a = static_cast<const uint16_t*>(x);
@@ -223,7 +285,7 @@ void backward(Call& c, const Gradients& g) {
   if (!products) return;
   if (g.need_dx) { // dz [M, C] times W: the sum runs over W's columns
     const int form = nk ? dense::kRowsKN : dense::kRowsNK;
-    const Plan plan = plan_rows(g.M, g.K, C, form, false);
+    const Plan plan = plan_rows(g.M, g.K, C, !nk, false, false, (nk ? g.K : C) % 8);
     Operand w = {static_cast<const uint16_t*>(g.w), g.ldw};
     if (plan.body > dense::kFew32) w = nk ? c.operand(g.w, g.ldw, C, g.K, 1, g.wide_w) : c.operand(g.w, g.ldw, g.K, C, 1, g.wide_w);
     Args a = {};
@@ -376,7 +438,8 @@ int pgemm_dense_query(int64_t M, int64_t N, int64_t K, int layout, int gated, in
   if (!body || !pieces || M < 1 || N < 1 || K < 1) return PGEMM_ERR_INVALID_ARG;
   const int rc = check(nullptr, M, N, K, layout, 0, gated, PGEMM_F16);
   if (rc != PGEMM_OK) return rc;
-  const Plan p = plan_rows(M, N, K, layout == PGEMM_B_NK ? dense::kRowsNK : dense::kRowsKN, gated);
+  const bool nk = layout == PGEMM_B_NK;
+  const Plan p = plan_rows(M, N, K, nk, gated, K % 8, (nk ? K : N) % 8);
   *body = p.body;
   *pieces = p.split;
   return PGEMM_OK;

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(512, 2) ping_kernel(Args a) {
       }
       return;
     }
-    const Epilogue<DT, GATED> epilogue(a);
+    const Epilogue<DT, GATED, true> epilogue(a); // N is a multiple of 8 here
 #pragma unroll
     for (int P = 0; P < (GATED ? 1 : 2); ++P) {
       float bv[8], bu[8];
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(512, 2) ping_kernel(Args a) {
         float v[8], w[8];
         eight(i, P, v);
         if constexpr (GATED) eight(i, 1, w);
-        if (m < a.M && n + 32 * P < a.N) epilogue.finish(m, n + 32 * P, v, w, bv, bu);
+        if (m < a.M && n + 32 * P < a.N) act::with_path(epilogue.k, [&](auto path) __attribute__((always_inline)) { epilogue.template finish<decltype(path)::value>(m, n + 32 * P, v, w, bv, bu); });
         __builtin_amdgcn_sched_barrier(0);
       }
     }

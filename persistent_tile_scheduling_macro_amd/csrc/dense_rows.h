@@ -38,7 +38,9 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
     v[j] = s[j / 4][j % 4];
     if constexpr (GATED) u[j] = s[2 + j / 4][j % 4];
   }
-  epilogue.finish((int)m, n, v, u, bv, bu);
+  act::with_path(epilogue.k, [&](auto path) __attribute__((always_inline)) {
+    epilogue.template finish<decltype(path)::value>((int)m, n, v, u, bv, bu);
+  });
 }
 
 // dz and the column sums of it. A workgroup takes 256 columns of y and a

@@ -28,18 +28,6 @@ using fast::read_b;
 using fast::static_for;
 using fast::wait_vmcnt;
 
-// load16_to_lds as an instruction of its own: of the builtin the compiler knows that it writes LDS, but not which stage,
-// and it waits ahead of a stage's reads for copies in flight into another, which leaves one step in flight (a 128 x 128
-// step then takes 0.55 us instead of 0.4). The kernel's own waits cover every copy; M0 holds the wave's LDS address.
-__device__ inline void copy16(intx4_t rsrc, uint32_t lds, uint32_t voffset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset), "s"(rsrc)
-               : "memory", "m0");
-}
-__device__ inline intx4_t rsrc_words(const void* base) { // make_rsrc's four words
-  const uint64_t p = (uint64_t)base;
-  return intx4_t{(int)(uint32_t)p, (int)((uint32_t)(p >> 32) & 0xFFFFu), 0x7FFFFFFF, kRsrcWord3};
-}
-
 template <int DT, int FORM, bool GATED, int BM, int S>
 __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
   constexpr int BN = 128, BK = 64;
@@ -261,7 +249,9 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
             *reinterpret_cast<floatx4_t*>(to + ld / 2 + 4 * h) = floatx4_t{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
         }
       } else {
-        epilogue.finish(m, n, v, w, bv, bu);
+        act::with_path(epilogue.k, [&](auto path) __attribute__((always_inline)) {
+          epilogue.template finish<decltype(path)::value>(m, n, v, w, bv, bu);
+        });
       }
     }
   }
