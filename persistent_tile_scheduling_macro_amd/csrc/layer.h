@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
     for (int i = 0; i < BLK * 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      if (i < x_loads) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
+      if (i == 0 || i < x_loads) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
   };
   floatx4_t acc[MB][BLK];
 #pragma unroll
@@ -220,24 +220,28 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
 // and eight experts of I = 1024: 17 us with eight waves, 12.5 us with 16).
 constexpr int down_waves(int blocks) { return blocks == 4 ? 8 : 16; }
 
-template <int DT, int MB>
+// The last step's chunks past a row's end are read as the row's last eight elements and put right on the way to LDS, and
+// the first eight rows of h are always read: of the loads on all paths the compiler counts the fewest, and with a path
+// that has none it would wait for every load in flight.
+// COLS: 16, or 8 where 16 would leave CUs idle (the MFMA's other eight repeat them). SHORT: I < 8.
+template <int DT, int MB, int COLS, bool SHORT>
 __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_kernel(Args a) {
   constexpr int WAVES = down_waves(MB), D = MB == 1 ? 4 : 2, XL = 2 * MB, RING = MB == 1 ? 8 : 4;
   static_assert(D < RING, "a ring entry lasts from an expert's first load to its last product");
-  constexpr int TURN = 2048 * (MB + 1), TOKENS = 16 * MB;
+  constexpr int WL = COLS / 8, TURN = 2048 * MB + 1024 * WL, TOKENS = 16 * MB;
   typedef typename fast::Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * TURN];
-  __shared__ floatx4_t s_out[WAVES][TOKENS * 4];     // [token][16 columns]
+  __shared__ floatx4_t s_out[WAVES][TOKENS * COLS / 4]; // [token][column]
   __shared__ int s_token[WAVES][RING][TOKENS];       // of an expert's rows
   __shared__ float s_share[WAVES][RING][TOKENS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, s = lane & 15, row = lane >> 3, chunk = lane & 7;
-  const int n0 = blockIdx.x * 16, H = a.H, I = a.I;
+  const int n0 = blockIdx.x * COLS, H = a.H, I = a.I;
   const int infos = a.awake[min(lane, a.most)]; // lane 0: how many; then the first experts
-  for (int i = lane; i < TOKENS * 4; i += 64) s_out[wave][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = lane; i < TOKENS * COLS / 4; i += 64) s_out[wave][i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
   const int awake = __builtin_amdgcn_readfirstlane(infos);
   const int steps = (I + 63) / 64;
   const int64_t units = (int64_t)awake * steps;
@@ -254,9 +258,9 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
     next_slot = a.slots[i];
     next_share = a.shares[i];
   };
-  const uint16_t* w[2];
+  const uint16_t* w[WL];
   int x[XL], l_rows = 0; // element offsets in h
-  struct Slot { u32x4 x[XL], w[2]; int loads; };
+  struct Slot { u32x4 x[XL], w[WL]; int loads, rest; };
   int left = mine;
   auto load = [&](Slot& t) __attribute__((always_inline)) {
     if (left <= 0) return;
@@ -266,12 +270,16 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
       l_rows = info >> 16;
       l_loads = (l_rows + 7) >> 3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) w[i] = a.w_out + ((int64_t)(info & 0xFFFF) * H + min(n0 + 8 * i + row, H - 1)) * I + 8 * chunk;
+      for (int i = 0; i < WL; ++i) w[i] = a.w_out + ((int64_t)(info & 0xFFFF) * H + min(n0 + 8 * i + row, H - 1)) * I + 8 * chunk;
     }
-    const int k0 = l_step * 64, rest = I - k0 - 8 * chunk;
-    const bool part = k0 + 64 > I;
+    const int at = min(l_step * 64, I - 8 - 8 * chunk); // from the lane's own chunk of the row's start
+    t.rest = I - l_step * 64;
+    auto chunk_of = [&](const uint16_t* p) __attribute__((always_inline)) {
+      if constexpr (SHORT) return load_upto(p, I - 8 * chunk, I);
+      else return moe::load8<moe::kAnyAddress>(p + at);
+    };
 #pragma unroll
-    for (int i = 0; i < 2; ++i) t.w[i] = part ? load_upto(w[i] + k0, rest, I) : moe::load8<moe::kAnyAddress>(w[i] + k0);
+    for (int i = 0; i < WL; ++i) t.w[i] = chunk_of(w[i]);
     if (fresh) { // the slots come in while the matrix is read
       const int slot = next_slot;
       const float share = next_share;
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
     t.loads = l_loads;
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      if (i < l_loads) t.x[i] = part ? load_upto(a.h + x[i] + k0, rest, I) : moe::load8<moe::kAnyAddress>(a.h + x[i] + k0);
+      if (i == 0 || i < l_loads) t.x[i] = chunk_of(a.h + x[i]);
     if (++l_step == steps) {
       l_step = 0;
       ++l_at;
@@ -306,8 +314,8 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
     for (int b = 0; b < MB; ++b) {
       const int token = s_token[wave][c_at % RING][16 * b + s];
       const float share = s_share[wave][c_at % RING][16 * b + s];
-      if (token >= 0) {
-        floatx4_t* o = &s_out[wave][token * 4 + g];
+      if (token >= 0 && 4 * g < COLS) {
+        floatx4_t* o = &s_out[wave][token * (COLS / 4) + g];
         floatx4_t v = *o;
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(share, acc[b][r], v[r]);
@@ -317,17 +325,28 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
     }
   };
   uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + 2048 * MB;
-  auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
+  auto multiply = [&](Slot& t) __attribute__((always_inline)) {
+    if (!SHORT && t.rest < 64) { // the row's end
+      const int own = t.rest - 8 * chunk;
+      auto cut = [&](u32x4 v) __attribute__((always_inline)) {
+        return own >= 8 ? v : own <= 0 ? u32x4{0, 0, 0, 0} : moe::shift_down(v, 8 - own);
+      };
+#pragma unroll
+      for (int i = 0; i < WL; ++i) t.w[i] = cut(t.w[i]);
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i < t.loads) t.x[i] = cut(t.x[i]);
+    }
     wave_fence(); // the last step's reads come first
 #pragma unroll
     for (int i = 0; i < XL; ++i)
       if (i < t.loads) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
+    for (int i = 0; i < WL; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
     wave_fence();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const frag_t f = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(s, 4 * h + g));
+      const frag_t f = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(s % COLS, 4 * h + g));
 #pragma unroll
       for (int b = 0; b < MB; ++b)
         if (2 * b < t.loads) {
@@ -359,20 +378,20 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
   }
   __syncthreads();
   const float* parts = reinterpret_cast<const float*>(s_out);
-  for (int i = tid; i < a.T * 16; i += WAVES * 64) {
-    const int c = n0 + (i & 15);
+  for (int i = tid; i < a.T * COLS; i += WAVES * 64) {
+    const int c = n0 + i % COLS;
     float v = parts[i];
 #pragma unroll
-    for (int o = 1; o < WAVES; ++o) v += parts[o * TOKENS * 16 + i];
-    if (c < H) a.out[(int64_t)(i >> 4) * H + c] = __builtin_bit_cast(uint16_t, to_out(v, (out_t*)nullptr));
+    for (int o = 1; o < WAVES; ++o) v += parts[o * TOKENS * COLS + i];
+    if (c < H) a.out[(int64_t)(i / COLS) * H + c] = __builtin_bit_cast(uint16_t, to_out(v, (out_t*)nullptr));
   }
 }
 
 typedef void (*kernel_fn)(Args);
 kernel_fn up_f16(bool gated, int blocks);
 kernel_fn up_bf16(bool gated, int blocks);
-kernel_fn down_f16(int blocks);
-kernel_fn down_bf16(int blocks);
+kernel_fn down_f16(int blocks, int columns, bool is_short);
+kernel_fn down_bf16(int blocks, int columns, bool is_short);
 
 template <int DT>
 kernel_fn pick_up(bool gated, int blocks) {
@@ -381,8 +400,10 @@ kernel_fn pick_up(bool gated, int blocks) {
   return gated ? up_kernel<DT, true, 4> : up_kernel<DT, false, 4>;
 }
 template <int DT>
-kernel_fn pick_down(int blocks) {
-  return blocks == 1 ? down_kernel<DT, 1> : blocks == 2 ? down_kernel<DT, 2> : down_kernel<DT, 4>;
+kernel_fn pick_down(int blocks, int columns, bool is_short) {
+  if (is_short) return blocks == 1 ? down_kernel<DT, 1, 16, true> : blocks == 2 ? down_kernel<DT, 2, 16, true> : down_kernel<DT, 4, 16, true>;
+  if (columns == 8) return blocks == 1 ? down_kernel<DT, 1, 8, false> : blocks == 2 ? down_kernel<DT, 2, 8, false> : down_kernel<DT, 4, 8, false>;
+  return blocks == 1 ? down_kernel<DT, 1, 16, false> : blocks == 2 ? down_kernel<DT, 2, 16, false> : down_kernel<DT, 4, 16, false>;
 }
 
 } // namespace layer

@@ -80,6 +80,7 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
   a.I = (int)I;
   a.act = act;
   const bool f16 = dtype == PGEMM_F16;
+  const int columns = I < 8 || H >= 16 * (int64_t)h->cus ? 16 : 8;
   hipError_t e = hipSuccess;
   for (int64_t t = 0; e == hipSuccess && t < T; t += layer::kTokens) { // more tokens than one pass has: each reads the matrices again
     a.T = (int)(T - t < layer::kTokens ? T - t : layer::kTokens);
@@ -92,7 +93,8 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
     e = enqueue(h->stream, dim3((unsigned)((I + 15) / 16), (unsigned)a.most), dim3(512),
                 f16 ? layer::up_f16(gated, blocks) : layer::up_bf16(gated, blocks), a);
     if (e == hipSuccess)
-      e = enqueue(h->stream, dim3((unsigned)((H + 15) / 16)), dim3(64 * layer::down_waves(blocks)), f16 ? layer::down_f16(blocks) : layer::down_bf16(blocks), a);
+      e = enqueue(h->stream, dim3((unsigned)((H + columns - 1) / columns)), dim3(64 * layer::down_waves(blocks)),
+                  f16 ? layer::down_f16(blocks, columns, I < 8) : layer::down_bf16(blocks, columns, I < 8), a);
   }
   return launch_status(h, e, "routed layer");
 }
