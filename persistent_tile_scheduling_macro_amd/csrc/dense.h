@@ -47,6 +47,18 @@ struct Args {
 // Columns of a piece's row: gate and up halves each a multiple of 8.
 __host__ __device__ inline int64_t part_ld(const Args& a, bool gated) { return (int64_t)(gated ? 2 : 1) * ((a.N + 7) / 8 * 8); }
 
+// Eight fp32 values to 16 bits, to the nearest, ties to even; a pair's conversion is one instruction for bf16.
+template <int DT>
+__device__ inline u32x4 pack(const float* f) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef typename Traits<DT>::out_t out2 __attribute__((ext_vector_type(2)));
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{f[2 * i], f[2 * i + 1]}), out2));
+  return v;
+}
+
 // Eight elements of a row, those past its end zeros.
 __device__ inline u32x4 load8_upto(const uint16_t* row, int64_t n, int64_t N) {
   return n + 8 <= N ? moe::load8<moe::kAnyAddress>(row + n) : moe::load_part(row + n, (int)(N - n));
@@ -66,8 +78,8 @@ struct Epilogue {
     return EVEN ? moe::load8<moe::kAnyAddress>(row + n) : load8_upto(row, n, a.N);
   }
   __device__ inline void store(uint16_t* row, int n, const float* v) const {
-    if constexpr (EVEN) moe::store8<moe::kAnyAddress>(row + n, moe::pack<DT>(v));
-    else moe::store_row<moe::kAnyAddress>(row, n, a.N, moe::pack<DT>(v));
+    if constexpr (EVEN) moe::store8<moe::kAnyAddress>(row + n, pack<DT>(v));
+    else moe::store_row<moe::kAnyAddress>(row, n, a.N, pack<DT>(v));
   }
 
   __device__ inline void bias_of(int n, float* bv, float* bu) const {
@@ -96,7 +108,7 @@ struct Epilogue {
       if constexpr (GATED) store(z + N, n, u);
     }
     u32x4 res = {0, 0, 0, 0};
-    if (a.residual) res = load8_upto(a.residual + m * a.ldr, n, N);
+    if (a.residual) res = load(a.residual + m * a.ldr, n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = act::value<PATH>(v[i], k);
@@ -108,7 +120,7 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += r[i];
     }
-    moe::store_row<moe::kAnyAddress>(a.c + (int64_t)m * N, n, (int)N, moe::pack<DT>(v));
+    moe::store_row<moe::kAnyAddress>(a.c + (int64_t)m * N, n, (int)N, pack<DT>(v));
   }
 };
 
@@ -172,15 +184,6 @@ struct ActGradArgs {
   int M, N, act;
   int stretches;
 };
-struct Kernels {
-  kernel_fn (*pick)(int body, int form, bool gated);
-  kernel_fn join[2];                 // by gated
-  void (*act_grad[2])(ActGradArgs);
-  void (*sum_columns)(ActGradArgs, int);
-};
-Kernels kernels_f16();
-Kernels kernels_bf16();
-
 // Rows of `halves` x `cols` elements, ld apart, to rows in which each half starts at a multiple of 8 and is
 // filled up with zeros.
 struct PadArgs {
@@ -190,6 +193,22 @@ struct PadArgs {
   int rows, cols, halves;
   int chunks; // of a half, eight elements each
 };
+// What goes into one launch ahead of the products: up to two operands moved, the column sums joined.
+struct SideArgs {
+  PadArgs pad[2];
+  int pad_blocks[2]; // 256 chunks each
+  ActGradArgs sums;
+  int C; // columns to sum, 64 a block; 0: none
+};
+
+struct Kernels {
+  kernel_fn (*pick)(int body, int form, bool gated);
+  kernel_fn join[2]; // by gated
+  void (*act_grad[2])(ActGradArgs);
+  void (*side)(SideArgs);
+};
+Kernels kernels_f16();
+Kernels kernels_bf16();
 
 } // namespace dense
 } // namespace pgemm

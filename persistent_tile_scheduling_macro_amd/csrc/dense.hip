@@ -12,16 +12,6 @@ constexpr int64_t kMaxSize = (int64_t)1 << 30;
 // Row strides up to which a tile's 32-bit offsets reach its last row (256 rows of 2-byte elements below 2^31).
 constexpr int64_t kMaxDirectStride = (int64_t)1 << 21;
 
-// One chunk of eight a thread.
-__global__ void __launch_bounds__(256) pad_rows_kernel(dense::PadArgs p) {
-  const int per = p.chunks * p.halves;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / per;
-  if (r >= p.rows) return;
-  const int at = (int)(i - r * per), h = at >= p.chunks ? 1 : 0, c = 8 * (at - h * p.chunks);
-  const dense::u32x4 v = dense::load8_upto(p.from + r * p.ld + (int64_t)h * p.cols, c, p.cols);
-  *reinterpret_cast<dense::u32x4*>(p.to + 8 * i) = v;
-}
-
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 
 // Scratch handed out piece by piece; with a null base it only counts.
@@ -162,15 +152,21 @@ struct Call {
     if (h && status == hipSuccess && grid > 0) status = enqueue(h->stream, dim3((unsigned)grid), dim3(threads), kernel, args...);
   }
 
-  // wide: the rows can be used as they are.
+  dense::SideArgs side = {}; // launched by prepare()
+  int pads = 0;
+
+  // wide: the rows can be used as they are; otherwise they are moved by prepare().
   Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int halves, bool wide) {
     Operand o = {static_cast<const uint16_t*>(p), ld, cols};
     if (wide) return o;
     const int64_t padded = round8(cols), chunks = padded / 8 * halves;
     uint16_t* to = scratch.take<uint16_t>(rows * padded * halves);
-    launch((rows * chunks + 255) / 256, 256, pad_rows_kernel,
-           dense::PadArgs{o.p, ld, to, (int)rows, (int)cols, halves, (int)(padded / 8)});
+    side.pad[pads] = {o.p, ld, to, (int)rows, (int)cols, halves, (int)(padded / 8)};
+    side.pad_blocks[pads++] = (int)((rows * chunks + 255) / 256);
     return {to, padded * halves, padded};
+  }
+  void prepare() {
+    launch((int64_t)side.pad_blocks[0] + side.pad_blocks[1] + (side.C + 63) / 64, 256, kernels.side, side);
   }
 
   void product(Args a, Plan plan, int form, bool gated) {
@@ -231,6 +227,7 @@ int forward(Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, boo
     a.b = wo.p;
     a.ldb = wo.ld;
     a.half = nk ? a.N * wo.ld : wo.half;
+    c.prepare();
   }
   c.product(a, plan, form, gated);
   return PGEMM_OK;
@@ -280,14 +277,21 @@ void backward(Call& c, const Gradients& g) {
     if (g.need_db) a.part = c.scratch.take<float>(a.stretches * C);
     if (c.h && c.status == hipSuccess && g.N > 0)
       c.status = enqueue(c.h->stream, dim3((unsigned)((g.N + 255) / 256), (unsigned)a.stretches), dim3(256), c.kernels.act_grad[g.gated], a);
-    if (g.need_db) c.launch((C + 63) / 64, 256, c.kernels.sum_columns, a, (int)C);
+    if (g.need_db) {
+      c.side.sums = a;
+      c.side.C = (int)C;
+    }
   }
+  // dx = dz [M, C] times W, the sum running over W's columns; dW = x^T dz or its transpose
+  const int form = nk ? dense::kRowsKN : dense::kRowsNK;
+  const Plan plan = plan_rows(g.M, g.K, C, !nk, false, false, (nk ? g.K : C) % 8);
+  Operand w = {static_cast<const uint16_t*>(g.w), g.ldw}, x = {static_cast<const uint16_t*>(g.x), g.ldx};
+  if (products && g.need_dx && plan.body > dense::kFew32)
+    w = nk ? c.operand(g.w, g.ldw, C, g.K, 1, g.wide_w) : c.operand(g.w, g.ldw, g.K, C, 1, g.wide_w);
+  if (products && g.need_dw) x = c.operand(g.x, g.ldx, g.M, g.K, 1, g.wide_x);
+  c.prepare();
   if (!products) return;
-  if (g.need_dx) { // dz [M, C] times W: the sum runs over W's columns
-    const int form = nk ? dense::kRowsKN : dense::kRowsNK;
-    const Plan plan = plan_rows(g.M, g.K, C, !nk, false, false, (nk ? g.K : C) % 8);
-    Operand w = {static_cast<const uint16_t*>(g.w), g.ldw};
-    if (plan.body > dense::kFew32) w = nk ? c.operand(g.w, g.ldw, C, g.K, 1, g.wide_w) : c.operand(g.w, g.ldw, g.K, C, 1, g.wide_w);
+  if (g.need_dx) {
     Args a = {};
     a.a = dz.p;
     a.lda = dz.ld;
@@ -300,7 +304,6 @@ void backward(Call& c, const Gradients& g) {
     c.product(a, plan, form, false);
   }
   if (g.need_dw) {
-    const Operand x = c.operand(g.x, g.ldx, g.M, g.K, 1, g.wide_x);
     Args a = {};
     a.a = nk ? dz.p : x.p;
     a.lda = nk ? dz.ld : x.ld;

@@ -33,7 +33,7 @@ kernel_fn pick(int body, int form, bool gated) {
 template <int DT>
 Kernels kernels() {
   return {pick<DT>, {join_kernel<DT, false>, join_kernel<DT, true>},
-          {act_grad_kernel<DT, false>, act_grad_kernel<DT, true>}, sum_columns_kernel<DT>};
+          {act_grad_kernel<DT, false>, act_grad_kernel<DT, true>}, side_kernel<DT>};
 }
 
 } // namespace dense

@@ -1,5 +1,5 @@
 // What stands around the linear layer's products: the pieces' sums joined, dz
-// with the bias' column sums.
+// with the bias' column sums, rows moved to padded ones.
 #pragma once
 
 #include "dense.h"
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
 // dz and the column sums of it. A workgroup takes 256 columns of y and a
 // stretch of the rows, a thread eight columns and every eighth row; the
 // threads' sums meet in LDS, the stretches' in `part` [stretches][C], which
-// sum_columns_kernel adds in order. dz rows are ldz apart (a multiple of 8),
+// side_kernel adds in order. dz rows are ldz apart (a multiple of 8),
 // filled up with zeros: they are the operands of the two products that follow.
 template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
         }
         if (a.dz) {
           uint16_t* to = a.dz + m * a.lddz;
-          moe::store_row<moe::kAnyAddress>(to, n, a.N, moe::pack<DT>(v));
-          if constexpr (GATED) moe::store_row<moe::kAnyAddress>(to + a.N, n, a.N, moe::pack<DT>(u));
+          moe::store_row<moe::kAnyAddress>(to, n, a.N, pack<DT>(v));
+          if constexpr (GATED) moe::store_row<moe::kAnyAddress>(to + a.N, n, a.N, pack<DT>(u));
           if (n + 8 >= a.N) // the row's last thread fills it up
             for (int64_t j = C; j < a.lddz; ++j) to[j] = 0;
         }
@@ -118,23 +118,37 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
   }
 }
 
-// db = the stretches' sums, four threads a column.
+// What the products wait for, in one launch (each would take some 5 us of its own): rows moved, one chunk of eight a
+// thread; db as the sum of the stretches' sums, four threads a column.
 template <int DT>
-__global__ void __launch_bounds__(256) sum_columns_kernel(ActGradArgs a, int C) {
+__global__ void __launch_bounds__(256) side_kernel(SideArgs a) {
   typedef typename Traits<DT>::out_t out_t;
   __shared__ float sums[4][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
-  float t = 0.0f;
-  if (col < C) {
-#pragma unroll 4
-    for (int j = part; j < a.stretches; j += 4) t += a.part[(int64_t)j * C + col];
+  int block = blockIdx.x;
+  for (int k = 0; k < 2; ++k) {
+    if (block < a.pad_blocks[k]) {
+      const PadArgs& p = a.pad[k];
+      const int per = p.chunks * p.halves;
+      const int64_t i = (int64_t)block * 256 + threadIdx.x, r = i / per;
+      if (r >= p.rows) return;
+      const int at = (int)(i - r * per), h = at >= p.chunks ? 1 : 0, c = 8 * (at - h * p.chunks);
+      const u32x4 v = load8_upto(p.from + r * p.ld + (int64_t)h * p.cols, c, p.cols);
+      *reinterpret_cast<u32x4*>(p.to + 8 * i) = v;
+      return;
+    }
+    block -= a.pad_blocks[k];
   }
-  sums[part][threadIdx.x & 63] = t;
+  const int i = threadIdx.x & 63, col = block * 64 + i, part = threadIdx.x >> 6;
+  float t = 0.0f;
+  if (col < a.C) {
+#pragma unroll 4
+    for (int j = part; j < a.sums.stretches; j += 4) t += a.sums.part[(int64_t)j * a.C + col];
+  }
+  sums[part][i] = t;
   __syncthreads();
-  if (part || col >= C) return;
-  const int i = threadIdx.x;
+  if (part || col >= a.C) return;
   t = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
-  a.db[col] = __builtin_bit_cast(uint16_t, to_out(t, (out_t*)nullptr));
+  a.sums.db[col] = __builtin_bit_cast(uint16_t, to_out(t, (out_t*)nullptr));
 }
 
 } // namespace dense
