@@ -183,6 +183,7 @@ struct ActGradArgs {
   uint16_t* db;
   int M, N, act;
   int stretches;
+  int stream; // N a multiple of 8: read dy and z past the memory-side cache
 };
 // Rows of `halves` x `cols` elements, ld apart, to rows in which each half starts at a multiple of 8 and is
 // filled up with zeros.

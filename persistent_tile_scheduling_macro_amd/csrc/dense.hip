@@ -235,7 +235,7 @@ int forward(Call& c, const void* x, int64_t ldx, const void* w, int64_t ldw, boo
 
 // Stretches of the rows whose column sums are formed separately: enough workgroups to fill the card, 16 rows each at least.
 int stretches_of(int64_t M, int64_t N) {
-  const int64_t blocks = (N + 255) / 256;
+  const int64_t blocks = (N + 511) / 512;
   int64_t s = 1024 / (blocks > 0 ? blocks : 1), most = (M + 15) / 16;
   if (s < 1) s = 1;
   if (s > most) s = most > 0 ? most : 1;
@@ -273,10 +273,11 @@ void backward(Call& c, const Gradients& g) {
     a.N = (int)g.N;
     a.act = g.act;
     a.stretches = stretches_of(g.M, g.N);
+    a.stream = g.N % 8 == 0 && 2 * g.M * (g.N + 2 * C) > (int64_t)256 << 20; // with dz, more than the cache's 256 MiB
     a.db = static_cast<uint16_t*>(g.db);
     if (g.need_db) a.part = c.scratch.take<float>(a.stretches * C);
     if (c.h && c.status == hipSuccess && g.N > 0)
-      c.status = enqueue(c.h->stream, dim3((unsigned)((g.N + 255) / 256), (unsigned)a.stretches), dim3(256), c.kernels.act_grad[g.gated], a);
+      c.status = enqueue(c.h->stream, dim3((unsigned)((g.N + 511) / 512), (unsigned)a.stretches), dim3(256), c.kernels.act_grad[g.gated], a);
     if (g.need_db) {
       c.side.sums = a;
       c.side.C = (int)C;

@@ -24,18 +24,19 @@ enum Act : int { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4, kAct
 enum Path : int { kCopy, kLogistic, kNormal };
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ inline float logistic(float u) { return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-1.44269504f * u)); }
 
 // Constants of one activation; uniform over a launch.
 struct Consts {
   int path;
   float floor;   // kCopy: what is below becomes 0 (relu: 0, none: -inf)
   float c0, c1;  // kLogistic
+  float e0, e1;  // the same times -log2(e), for exp2
 };
 __device__ inline Consts consts_of(int a) {
   const bool tanh_form = a == kGeluTanh;
   return {a == kGelu ? kNormal : a == kSilu || tanh_form ? kLogistic : kCopy, a == kRelu ? 0.0f : -__builtin_huge_valf(),
-          tanh_form ? 1.59576912f : 1.0f, tanh_form ? 0.0713548163f : 0.0f};
+          tanh_form ? 1.59576912f : 1.0f, tanh_form ? 0.0713548163f : 0.0f,
+          tanh_form ? -2.30220818f : -1.44269504f, tanh_form ? -0.102943240f : 0.0f};
 }
 
 // Phi(x) and exp(-x^2 / 2).
@@ -60,31 +61,31 @@ __device__ inline float value(float x, const Consts& c) {
   if constexpr (PATH == kCopy) {
     return x < c.floor ? 0.0f : x;
   } else if constexpr (PATH == kLogistic) {
-    return x * logistic(x * __builtin_fmaf(c.c1 * x, x, c.c0));
+    return x * __builtin_amdgcn_rcpf(1.0f + exp2_fast(x * __builtin_fmaf(c.e1 * x, x, c.e0)));
   } else {
     float bell;
     return x * normal_cdf(x, &bell);
   }
 }
 
-// Value and slope. Past |x| = 100 every slope is 0 or 1 in fp32, and the products there would leave its range.
+// Value and slope. (The backward pass over 8192 x 8192 pre-activations is bound by these instructions, not by their
+// bytes, so they are counted: the square is kept below 10^4, where every s is 0 or 1, instead of clamping x.)
 template <int PATH>
 __device__ inline float value_and_slope(float x, const Consts& c, float* slope) {
   if constexpr (PATH == kCopy) {
     *slope = c.floor < 0.0f || x > 0.0f ? 1.0f : x != x ? x : 0.0f;
     return x < c.floor ? 0.0f : x;
+  } else if constexpr (PATH == kLogistic) {
+    const float q = __builtin_fminf(x * x, 1e4f);
+    const float p = __builtin_amdgcn_rcpf(1.0f + exp2_fast(x * __builtin_fmaf(c.e1, q, c.e0)));
+    const float value = x * p;
+    *slope = __builtin_fmaf(value * (1.0f - p), __builtin_fmaf(3.0f * c.c1, q, c.c0), p);
+    return value;
   } else {
-    const float s = x > 100.0f ? 100.0f : x < -100.0f ? -100.0f : x;
-    if constexpr (PATH == kLogistic) {
-      const float p = logistic(s * __builtin_fmaf(c.c1 * s, s, c.c0));
-      *slope = __builtin_fmaf(s * p * (1.0f - p), __builtin_fmaf(3.0f * c.c1 * s, s, c.c0), p);
-      return x * p;
-    } else {
-      float bell;
-      const float p = normal_cdf(s, &bell);
-      *slope = __builtin_fmaf(0.39894228f * s, bell, p);
-      return x * p;
-    }
+    float bell;
+    const float p = normal_cdf(x, &bell);
+    *slope = __builtin_fmaf(0.39894228f * x, bell, p);
+    return x * p;
   }
 }
 

@@ -43,16 +43,18 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
   });
 }
 
-// dz and the column sums of it. A workgroup takes 256 columns of y and a
-// stretch of the rows, a thread eight columns and every eighth row; the
+// dz and the column sums of it. A workgroup takes 512 columns of y (a wave's
+// reads are 1 KiB of a row) and a stretch of the rows, a thread eight columns and every fourth row; the
 // threads' sums meet in LDS, the stretches' in `part` [stretches][C], which
 // side_kernel adds in order. dz rows are ldz apart (a multiple of 8),
 // filled up with zeros: they are the operands of the two products that follow.
+// dy and z that the memory-side cache cannot hold beside dz are read past it (8192 x 8192 with dz: 97 us, kept 109; 4096 x
+// 2048 26 us and 22), 4.1 TB/s; with 256 columns a workgroup the column sums alone took 61 us, now 49.
 template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
-  __shared__ float sums[8][GATED ? 2 : 1][256];
-  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
-  const int n = blockIdx.x * 256 + 8 * lane;
+  __shared__ float sums[4][GATED ? 2 : 1][512];
+  const int tid = threadIdx.x, lane = tid & 63, strip = tid >> 6;
+  const int n = blockIdx.x * 512 + 8 * lane;
   const int64_t C = GATED ? 2 * (int64_t)a.N : a.N;
   const int lo = (int)((int64_t)a.M * blockIdx.y / a.stretches), hi = (int)((int64_t)a.M * (blockIdx.y + 1) / a.stretches);
   const act::Consts k = act::consts_of(a.act);
@@ -60,45 +62,61 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
   float sv[8], su[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.0f;
-  if (live) {
-    act::with_path(k, [&](auto path) __attribute__((always_inline)) {
-      constexpr int PATH = decltype(path)::value;
-#pragma unroll 2
-      for (int m = lo + strip; m < hi; m += 8) {
-        float d[8], v[8], u[8];
-        moe::unpack<DT>(load8_upto(a.dy + m * a.lddy, n, a.N), d);
-        if (a.z) {
-          moe::unpack<DT>(load8_upto(a.z + m * C, n, a.N), v);
-          if constexpr (GATED) moe::unpack<DT>(load8_upto(a.z + m * C + a.N, n, a.N), u);
+  // A row's eight columns: d the gradient, v (and u) the pre-activations, then dz.
+  auto one_row = [&](auto path, auto with_z, int m, u32x4 dr, u32x4 vr, u32x4 ur) __attribute__((always_inline)) {
+    float d[8], v[8], u[8];
+    moe::unpack<DT>(dr, d);
+    if constexpr (decltype(with_z)::value) {
+      moe::unpack<DT>(vr, v);
+      if constexpr (GATED) moe::unpack<DT>(ur, u);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float slope;
-            const float value = act::value_and_slope<PATH>(v[i], k, &slope);
-            if constexpr (GATED) {
-              v[i] = d[i] * u[i] * slope;
-              u[i] = d[i] * value;
-            } else {
-              v[i] = d[i] * slope;
-            }
-          }
+      for (int i = 0; i < 8; ++i) {
+        float slope;
+        const float value = act::value_and_slope<decltype(path)::value>(v[i], k, &slope);
+        if constexpr (GATED) {
+          v[i] = d[i] * u[i] * slope;
+          u[i] = d[i] * value;
         } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = d[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sv[i] += v[i];
-          if constexpr (GATED) su[i] += u[i];
-        }
-        if (a.dz) {
-          uint16_t* to = a.dz + m * a.lddz;
-          moe::store_row<moe::kAnyAddress>(to, n, a.N, pack<DT>(v));
-          if constexpr (GATED) moe::store_row<moe::kAnyAddress>(to + a.N, n, a.N, pack<DT>(u));
-          if (n + 8 >= a.N) // the row's last thread fills it up
-            for (int64_t j = C; j < a.lddz; ++j) to[j] = 0;
+          v[i] = d[i] * slope;
         }
       }
-    });
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = d[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sv[i] += v[i];
+      if constexpr (GATED) su[i] += u[i];
+    }
+    if (a.dz) {
+      uint16_t* to = a.dz + m * a.lddz;
+      moe::store_row<moe::kAnyAddress>(to, n, a.N, pack<DT>(v));
+      if constexpr (GATED) moe::store_row<moe::kAnyAddress>(to + a.N, n, a.N, pack<DT>(u));
+      if (n + 8 >= a.N) // the row's last thread fills it up
+        for (int64_t j = C; j < a.lddz; ++j) to[j] = 0;
+    }
+  };
+  auto rows = [&](auto path, auto with_z, auto stream) __attribute__((always_inline)) {
+    auto eight = [&](const uint16_t* row) __attribute__((always_inline)) {
+      if constexpr (decltype(stream)::value) return __builtin_nontemporal_load(reinterpret_cast<const moe::u32x4_any*>(row + n));
+      else return load8_upto(row, n, a.N);
+    };
+    constexpr bool Z = decltype(with_z)::value;
+    const u32x4 none = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int64_t m = lo + strip; m < hi; m += 4)
+      one_row(path, with_z, (int)m, eight(a.dy + m * a.lddy), Z ? eight(a.z + m * C) : none, Z && GATED ? eight(a.z + m * C + a.N) : none);
+  };
+  if (live) {
+    if (GATED || a.z) {
+      act::with_path(k, [&](auto path) __attribute__((always_inline)) {
+        if (a.stream) rows(path, std::true_type{}, std::true_type{});
+        else rows(path, std::true_type{}, std::false_type{});
+      });
+    } else {
+      rows(std::integral_constant<int, act::kCopy>{}, std::false_type{}, std::false_type{});
+    }
   }
   if (!a.part) return;
 #pragma unroll
@@ -107,14 +125,17 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
     if constexpr (GATED) sums[strip][1][8 * lane + i] = su[i];
   }
   __syncthreads();
-  const int col = blockIdx.x * 256 + tid;
-  if (col >= a.N) return;
 #pragma unroll
-  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-    float t = 0.0f;
+  for (int c = tid; c < 512; c += 256) {
+    const int col = blockIdx.x * 512 + c;
+    if (col >= a.N) break;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t += sums[j][h][tid];
-    a.part[(int64_t)blockIdx.y * C + (int64_t)h * a.N + col] = t;
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t += sums[j][h][c];
+      a.part[(int64_t)blockIdx.y * C + (int64_t)h * a.N + col] = t;
+    }
   }
 }
 
