@@ -8,17 +8,35 @@ namespace {
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace of a pass: the plan of the awake experts, then h.
-struct Parts { int64_t awake, slots, shares, h, bytes; };
-Parts parts_of(int64_t T, int64_t k, int64_t E, int64_t I) {
-  const int64_t t = T < layer::kTokens ? T : layer::kTokens, n = t * k, most = E < n ? E : n;
+// Blocks of 16 rows in a group, by the mean number of tokens that take an awake expert (n slots among E experts leave
+// E (1 - 1/E)^n of them asleep): up to 6 rows rarely exceed 16, up to 16 rarely 32.
+int blocks_of(int64_t T, int64_t k, int64_t E) {
+  const double n = (double)T * k, mean = n / (E * (1 - __builtin_exp(-n / E)));
+  if (T <= 16 || mean <= 6) return 1;
+  return T <= 32 || mean <= 16 ? 2 : 4;
+}
+
+// Workspace of a pass of T tokens.
+struct Parts { int64_t slots, shares, arrived, parts, h, bytes, most, sharers; };
+Parts parts_of(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int cus) {
+  const int64_t t = T < layer::kTokens ? T : layer::kTokens, n = t * k, tiles = (H + 15) / 16;
+  const int blocks = blocks_of(t, k, E);
   Parts p = {};
-  p.slots = p.awake + round256((most + 1) * 4);
-  p.shares = p.slots + round256(most * layer::kTokens * 4);
-  p.h = p.shares + round256(most * layer::kTokens * 4);
+  p.most = (E < n ? E : n) + n / (16 * blocks); // whole groups and each expert's last
+  const int64_t room = (E < n ? E : n) + n / 16; // a last pass of fewer tokens may have smaller groups, and more of them
+  // Workgroups that share 16 columns of out: enough for every CU, each wave with two steps at least.
+  const int64_t steps = p.most * ((I + 63) / 64), fill = tiles > 0 ? cus / tiles : 1, long_enough = steps / (2 * layer::down_waves(blocks));
+  p.sharers = fill < long_enough ? fill : long_enough;
+  p.sharers = p.sharers < 1 ? 1 : p.sharers > 16 ? 16 : p.sharers;
+  p.slots = round256((room + 1) * 4);
+  p.shares = p.slots + round256(room * layer::kTokens * 4);
+  p.arrived = p.shares + round256(room * layer::kTokens * 4);
+  p.parts = p.arrived + round256(tiles * 4);
+  p.h = p.parts + round256(tiles * p.sharers * t * 64);
   p.bytes = p.h + round256(n * I * 2);
   return p;
 }
+constexpr int kCus = 256; // the workspace is the same whatever device runs it
 
 int check(pgemm_ctx* h, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (T < 0 || k < 1 || E < 1 || H < 0 || I < 0)
@@ -39,7 +57,7 @@ int pgemm_moe_layer_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_
   if (!bytes) return PGEMM_ERR_INVALID_ARG;
   *bytes = 0;
   const int rc = check(nullptr, T, k, E, H, I);
-  if (rc == PGEMM_OK && T > 0) *bytes = parts_of(T, k, E, I).bytes;
+  if (rc == PGEMM_OK && T > 0) *bytes = parts_of(T, k, E, H, I, kCus).bytes;
   return rc;
 }
 
@@ -57,7 +75,7 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
   if (dtype != PGEMM_F16 && dtype != PGEMM_BF16) return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
   if (T == 0 || H == 0) return PGEMM_OK;
   if (!x || !ids || !weights || !out || (I > 0 && (!w_in || !w_out))) return fail(h, PGEMM_ERR_INVALID_ARG, "a pointer is NULL");
-  const Parts p = parts_of(T, k, E, I);
+  const Parts p = parts_of(T, k, E, H, I, kCus);
   if (!work || work_bytes < p.bytes || (uintptr_t)work % 16)
     return fail(h, PGEMM_ERR_INVALID_ARG, "workspace of %lld bytes at %p, %lld at a multiple of 16 are needed", (long long)work_bytes,
                 work, (long long)p.bytes);
@@ -71,16 +89,17 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
   a.w_in = static_cast<const uint16_t*>(w_in);
   a.w_out = static_cast<const uint16_t*>(w_out);
   a.h = reinterpret_cast<uint16_t*>(base + p.h);
-  a.awake = reinterpret_cast<int*>(base + p.awake);
+  a.groups = reinterpret_cast<int*>(base);
   a.slots = reinterpret_cast<int*>(base + p.slots);
   a.shares = reinterpret_cast<float*>(base + p.shares);
+  a.arrived = reinterpret_cast<int*>(base + p.arrived);
+  a.parts = reinterpret_cast<float*>(base + p.parts);
   a.k = (int)k;
   a.E = (int)E;
   a.H = (int)H;
   a.I = (int)I;
   a.act = act;
   const bool f16 = dtype == PGEMM_F16;
-  const int columns = I < 8 || H >= 16 * (int64_t)h->cus ? 16 : 8;
   hipError_t e = hipSuccess;
   for (int64_t t = 0; e == hipSuccess && t < T; t += layer::kTokens) { // more tokens than one pass has: each reads the matrices again
     a.T = (int)(T - t < layer::kTokens ? T - t : layer::kTokens);
@@ -88,13 +107,15 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
     a.ids = static_cast<const char*>(ids) + t * k * (a.ids64 ? 8 : 4);
     a.weights = weights + t * k;
     a.out = static_cast<uint16_t*>(out) + t * H;
-    const int blocks = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-    a.most = (int)(E < a.T * k ? E : a.T * k);
+    const Parts q = parts_of(a.T, k, E, H, I, kCus); // laid out like the first pass
+    const int blocks = blocks_of(a.T, k, E);
+    a.most = (int)q.most;
+    a.sharers = (int)(q.sharers < p.sharers ? q.sharers : p.sharers);
     e = enqueue(h->stream, dim3((unsigned)((I + 15) / 16), (unsigned)a.most), dim3(512),
                 f16 ? layer::up_f16(gated, blocks) : layer::up_bf16(gated, blocks), a);
     if (e == hipSuccess)
-      e = enqueue(h->stream, dim3((unsigned)((H + columns - 1) / columns)), dim3(64 * layer::down_waves(blocks)),
-                  f16 ? layer::down_f16(blocks, columns, I < 8) : layer::down_bf16(blocks, columns, I < 8), a);
+      e = enqueue(h->stream, dim3((unsigned)((H + 15) / 16), (unsigned)a.sharers), dim3(64 * layer::down_waves(blocks)),
+                  f16 ? layer::down_f16(blocks, I < 8) : layer::down_bf16(blocks, I < 8), a);
   }
   return launch_status(h, e, "routed layer");
 }
