@@ -64,8 +64,11 @@ __device__ inline void wave_fence() { // LDS serves a wave in order: only the co
   __builtin_amdgcn_wave_barrier();
 }
 
-template <int DT, bool GATED, int MB>
-__global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
+// LOOP: several turns of 16 columns a workgroup, for short rows, where finding the group (some 3 us) is most of a turn's
+// work (21 experts, 286 x 4056: 86 us, looped 66; 128 experts, 1024 x 512 gated: 45 and 41). With long rows other workgroups' turns overlap it, and
+// turns one after another do not (32 experts, 4096 x 2048 gated: 288 us and 326).
+template <int DT, bool GATED, int MB, bool LOOP>
+__global__ void __launch_bounds__(512, MB == 4 || (LOOP && MB == 2) ? 2 : 4) up_kernel(Args a) {
   constexpr int WAVES = 8, BLK = GATED ? 2 : 1, D = MB > 1 ? 2 : GATED ? 3 : 4, XL = 2 * MB;
   constexpr int TURN = 2048 * (MB + BLK), JOIN = BLK * MB * 1024;
   typedef typename fast::Frag<DT>::t frag_t;
@@ -77,7 +80,6 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g = lane >> 4, s = lane & 15;
   const int n = a.T * a.k, H = a.H, I = a.I;
   const bool writes = blockIdx.x == 0;
 
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
 
   // every wave finds the rows for itself: lane t looks through its token's choices, and the tokens that
   // have one move to the front
-  const int n0 = blockIdx.x * 16, row = lane >> 3, chunk = lane & 7;
+  const int row = lane >> 3, chunk = lane & 7;
   int slot = -1;
   float share = 0.0f;
   if (lane < a.T) {
@@ -146,94 +148,110 @@ __global__ void __launch_bounds__(512, 4) up_kernel(Args a) {
 
   // ---- the product
   const int x_loads = __builtin_amdgcn_readfirstlane((rows + 7) >> 3), blocks = (x_loads + 1) >> 1;
-  const uint16_t* x[XL];
+  const uint16_t* x_kept[XL];
 #pragma unroll
-  for (int i = 0; i < XL; ++i) x[i] = a.x + __shfl(slot_at, first_row + min(8 * i + row, rows - 1)) / a.k * a.ldx + 8 * chunk;
-  const uint16_t* w[BLK * 2];
-#pragma unroll
-  for (int i = 0; i < BLK * 2; ++i)
-    w[i] = a.w_in + ((int64_t)e * I * BLK + (i >= 2 ? I : 0) + min(n0 + 8 * (i & 1) + row, I - 1)) * H + 8 * chunk;
-  struct Slot { u32x4 x[XL], w[BLK * 2]; };
-  auto load = [&](Slot& t, int step) __attribute__((always_inline)) {
-    const int64_t k0 = (int64_t)step * 64;
-#pragma unroll
-    for (int i = 0; i < BLK * 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-      if (i == 0 || i < x_loads) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
-  };
-  floatx4_t acc[MB][BLK];
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int c = 0; c < BLK; ++c) acc[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-  uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + 2048 * MB;
-  auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
-    wave_fence(); // the last step's reads come first
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-      if (i < x_loads) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
-#pragma unroll
-    for (int i = 0; i < BLK * 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
-    wave_fence();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      frag_t f[BLK];
-#pragma unroll
-      for (int c = 0; c < BLK; ++c) f[c] = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(16 * c + s, 4 * h + g));
-#pragma unroll
-      for (int b = 0; b < MB; ++b)
-        if (b < blocks) {
-          // an odd number of loads leaves the block's upper half to repeat its lower one
-          const int r = 16 * b + (2 * b + 1 < x_loads ? s : s & 7);
-          const frag_t xf = *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(r, 4 * h + g));
-#pragma unroll
-          for (int c = 0; c < BLK; ++c) acc[b][c] = mfma(f[c], xf, acc[b][c]);
-        }
-    }
-  };
-  const int whole = H / 64, mine = (whole - wave + WAVES - 1) / WAVES;
-  dense::stream_steps<D, Slot>(
-      mine, [&](Slot& t, int i) __attribute__((always_inline)) { load(t, wave + WAVES * i); }, multiply);
-  if (whole * 64 < H && wave == whole % WAVES) { // the partial step, zeros past H
-    const int k0 = whole * 64;
-    Slot t;
-#pragma unroll
-    for (int i = 0; i < BLK * 2; ++i) t.w[i] = load_upto(w[i] + k0, H - k0 - 8 * chunk, H);
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-      if (i < x_loads) t.x[i] = load_upto(x[i] + k0, H - k0 - 8 * chunk, H);
-    multiply(t);
-  }
-
-  __syncthreads(); // every wave is through with its part of the LDS
-  floatx4_t* join = reinterpret_cast<floatx4_t*>(lds);
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int c = 0; c < BLK; ++c) join[(wave * BLK * MB + c * MB + b) * 64 + lane] = acc[b][c];
-  __syncthreads();
-  const int b = tid >> 6, m = 16 * b + s;
-  if (b >= MB || m >= rows) return;
-  floatx4_t v = join[tid], u = floatx4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int o = 1; o < WAVES; ++o) v += join[o * BLK * MB * 64 + tid];
-  if constexpr (GATED) {
-    u = join[MB * 64 + tid];
-#pragma unroll
-    for (int o = 1; o < WAVES; ++o) u += join[o * BLK * MB * 64 + MB * 64 + tid];
-  }
+  for (int i = 0; i < XL; ++i) x_kept[i] = a.x + __shfl(slot_at, first_row + min(8 * i + row, rows - 1)) / a.k * a.ldx + 8 * chunk;
   const act::Consts k = act::consts_of(a.act);
-  uint16_t* to = a.h + (int64_t)s_row[m] * I;
+  int n0 = blockIdx.x * 16;
+  do {
+    // opaque, or the turn's addresses would all be kept in registers from turn to turn, and spilled
+    int lane_v = tid & 63;
+    asm volatile("" : "+v"(lane_v));
+    const int row = lane_v >> 3, chunk = lane_v & 7, g = lane_v >> 4, s = lane_v & 15;
+    const uint16_t* x[XL];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int c = n0 + 4 * g + r;
-    if (c >= I) continue;
-    float y = v[r];
-    act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
-    if constexpr (GATED) y *= u[r];
-    to[c] = __builtin_bit_cast(uint16_t, to_out(y, (out_t*)nullptr));
-  }
+    for (int i = 0; i < XL; ++i) {
+      x[i] = x_kept[i];
+      asm volatile("" : "+v"(x[i]));
+    }
+    const uint16_t* w[BLK * 2];
+#pragma unroll
+    for (int i = 0; i < BLK * 2; ++i)
+      w[i] = a.w_in + ((int64_t)e * I * BLK + (i >= 2 ? I : 0) + min(n0 + 8 * (i & 1) + row, I - 1)) * H + 8 * chunk;
+    struct Slot { u32x4 x[XL], w[BLK * 2]; };
+    auto load = [&](Slot& t, int step) __attribute__((always_inline)) {
+      const int64_t k0 = (int64_t)step * 64;
+#pragma unroll
+      for (int i = 0; i < BLK * 2; ++i) t.w[i] = moe::load8<moe::kAnyAddress>(w[i] + k0);
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i == 0 || i < x_loads) t.x[i] = moe::load8<moe::kAnyAddress>(x[i] + k0);
+    };
+    floatx4_t acc[MB][BLK];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int c = 0; c < BLK; ++c) acc[b][c] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    uint8_t *turn_x = lds + wave * TURN, *turn_w = turn_x + 2048 * MB;
+    auto multiply = [&](const Slot& t) __attribute__((always_inline)) {
+      wave_fence(); // the last step's reads come first
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i < x_loads) *reinterpret_cast<u32x4*>(turn_x + turn_at<128>(8 * i + row, chunk)) = t.x[i];
+#pragma unroll
+      for (int i = 0; i < BLK * 2; ++i) *reinterpret_cast<u32x4*>(turn_w + turn_at<128>(8 * i + row, chunk)) = t.w[i];
+      wave_fence();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        frag_t f[BLK];
+#pragma unroll
+        for (int c = 0; c < BLK; ++c) f[c] = *reinterpret_cast<const frag_t*>(turn_w + turn_at<128>(16 * c + s, 4 * h + g));
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          if (b < blocks) {
+            // an odd number of loads leaves the block's upper half to repeat its lower one
+            const int r = 16 * b + (2 * b + 1 < x_loads ? s : s & 7);
+            const frag_t xf = *reinterpret_cast<const frag_t*>(turn_x + turn_at<128>(r, 4 * h + g));
+#pragma unroll
+            for (int c = 0; c < BLK; ++c) acc[b][c] = mfma(f[c], xf, acc[b][c]);
+          }
+      }
+    };
+    const int whole = H / 64, mine = (whole - wave + WAVES - 1) / WAVES;
+    dense::stream_steps<D, Slot>(
+        mine, [&](Slot& t, int i) __attribute__((always_inline)) { load(t, wave + WAVES * i); }, multiply);
+    if (whole * 64 < H && wave == whole % WAVES) { // the partial step, zeros past H
+      const int k0 = whole * 64;
+      Slot t;
+#pragma unroll
+      for (int i = 0; i < BLK * 2; ++i) t.w[i] = load_upto(w[i] + k0, H - k0 - 8 * chunk, H);
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+        if (i < x_loads) t.x[i] = load_upto(x[i] + k0, H - k0 - 8 * chunk, H);
+      multiply(t);
+    }
+
+    __syncthreads(); // every wave is through with its part of the LDS
+    floatx4_t* join = reinterpret_cast<floatx4_t*>(lds);
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int c = 0; c < BLK; ++c) join[(wave * BLK * MB + c * MB + b) * 64 + lane] = acc[b][c];
+    __syncthreads();
+    const int b = tid >> 6, m = 16 * b + s;
+    if (b < MB && m < rows) {
+    floatx4_t v = join[tid], u = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int o = 1; o < WAVES; ++o) v += join[o * BLK * MB * 64 + tid];
+    if constexpr (GATED) {
+      u = join[MB * 64 + tid];
+#pragma unroll
+      for (int o = 1; o < WAVES; ++o) u += join[o * BLK * MB * 64 + MB * 64 + tid];
+    }
+    uint16_t* to = a.h + (int64_t)s_row[m] * I;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int c = n0 + 4 * g + r;
+      if (c >= I) continue;
+      float y = v[r];
+      act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
+      if constexpr (GATED) y *= u[r];
+      to[c] = __builtin_bit_cast(uint16_t, to_out(y, (out_t*)nullptr));
+    }
+    }
+    if constexpr (LOOP) __syncthreads(); // the next turn writes the LDS that this one read
+    n0 += gridDim.x * 16;
+  } while (LOOP && n0 < I);
 }
 
 // Waves of a workgroup of down_kernel, as many as LDS holds: there are few workgroups (16 columns of 2048 rows and eight
@@ -426,16 +444,19 @@ __global__ void __launch_bounds__(64 * down_waves(MB), MB == 4 ? 2 : 4) down_ker
 }
 
 typedef void (*kernel_fn)(Args);
-kernel_fn up_f16(bool gated, int blocks);
-kernel_fn up_bf16(bool gated, int blocks);
+kernel_fn up_f16(bool gated, int blocks, bool loop);
+kernel_fn up_bf16(bool gated, int blocks, bool loop);
 kernel_fn down_f16(int blocks, bool is_short);
 kernel_fn down_bf16(int blocks, bool is_short);
 
+template <int DT, bool GATED, bool LOOP>
+kernel_fn pick_up_blocks(int blocks) {
+  return blocks == 1 ? up_kernel<DT, GATED, 1, LOOP> : blocks == 2 ? up_kernel<DT, GATED, 2, LOOP> : up_kernel<DT, GATED, 4, LOOP>;
+}
 template <int DT>
-kernel_fn pick_up(bool gated, int blocks) {
-  if (blocks == 1) return gated ? up_kernel<DT, true, 1> : up_kernel<DT, false, 1>;
-  if (blocks == 2) return gated ? up_kernel<DT, true, 2> : up_kernel<DT, false, 2>;
-  return gated ? up_kernel<DT, true, 4> : up_kernel<DT, false, 4>;
+kernel_fn pick_up(bool gated, int blocks, bool loop) {
+  if (loop) return gated ? pick_up_blocks<DT, true, true>(blocks) : pick_up_blocks<DT, false, true>(blocks);
+  return gated ? pick_up_blocks<DT, true, false>(blocks) : pick_up_blocks<DT, false, false>(blocks);
 }
 template <int DT>
 kernel_fn pick_down(int blocks, bool is_short) {

@@ -111,8 +111,10 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
     const int blocks = blocks_of(a.T, k, E);
     a.most = (int)q.most;
     a.sharers = (int)(q.sharers < p.sharers ? q.sharers : p.sharers);
-    e = enqueue(h->stream, dim3((unsigned)((I + 15) / 16), (unsigned)a.most), dim3(512),
-                f16 ? layer::up_f16(gated, blocks) : layer::up_bf16(gated, blocks), a);
+    const int64_t tiles = (I + 15) / 16, fill = (512 + a.most - 1) / a.most; // two workgroups a CU
+    const bool loop = H <= 1024 && fill < tiles;
+    e = enqueue(h->stream, dim3((unsigned)(loop ? fill : tiles), (unsigned)a.most), dim3(512),
+                f16 ? layer::up_f16(gated, blocks, loop) : layer::up_bf16(gated, blocks, loop), a);
     if (e == hipSuccess)
       e = enqueue(h->stream, dim3((unsigned)((H + 15) / 16), (unsigned)a.sharers), dim3(64 * layer::down_waves(blocks)),
                   f16 ? layer::down_f16(blocks, I < 8) : layer::down_bf16(blocks, I < 8), a);

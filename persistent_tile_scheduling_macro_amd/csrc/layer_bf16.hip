@@ -3,7 +3,7 @@
 
 namespace pgemm {
 namespace layer {
-kernel_fn up_bf16(bool gated, int blocks) { return pick_up<kBF16>(gated, blocks); }
+kernel_fn up_bf16(bool gated, int blocks, bool loop) { return pick_up<kBF16>(gated, blocks, loop); }
 kernel_fn down_bf16(int blocks, bool is_short) { return pick_down<kBF16>(blocks, is_short); }
 } // namespace layer
 } // namespace pgemm

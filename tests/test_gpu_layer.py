@@ -69,7 +69,7 @@ def check(out, x, ids, weights, w_in, w_out, act, gated):
 SIZES = [(1, 1, 1, 64, 64), (1, 8, 64, 256, 128), (3, 2, 5, 33, 17), (8, 4, 6, 136, 72), (9, 3, 13, 1021, 517), (11, 3, 13, 1000, 520),
          (16, 8, 16, 512, 256), (17, 2, 4, 200, 333), (24, 8, 300, 64, 96), (32, 4, 8, 1024, 512), (33, 5, 7, 129, 65),
          (40, 2, 2, 512, 264), (64, 8, 64, 320, 192), (64, 32, 40, 72, 40), (64, 1, 1024, 48, 40), (65, 2, 4, 128, 64), (5, 2, 3, 40, 7), (20, 2, 3, 7, 5), (50, 3, 5, 9, 1), (4, 2, 3, 1, 8), (3, 4, 90, 64, 8),
-         (6, 2, 4, 4104, 72), (36, 6, 21, 286, 1500), (46, 3, 9, 944, 600), (2, 2, 6, 16, 4000), (64, 4, 4, 100, 1000), (127, 2, 5, 80, 700), (30, 4, 100, 4096, 136), (64, 3, 7, 4100, 65),
+         (6, 2, 4, 4104, 72), (36, 6, 21, 286, 1500), (46, 3, 9, 944, 600), (2, 2, 6, 16, 4000), (64, 4, 4, 100, 1000), (127, 2, 5, 80, 700), (60, 2, 3, 72, 2100), (20, 8, 90, 130, 300), (30, 2, 4, 264, 3500), (30, 4, 100, 4096, 136), (64, 3, 7, 4100, 65),
          (150, 6, 12, 96, 100)]
 
 
