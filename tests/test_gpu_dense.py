@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import dense_cases as cases
 import dense_refs as refs
 
 pytestmark = pytest.mark.gpu
@@ -214,3 +215,112 @@ def test_another_stream(dense):
         got = [dense.matmul(x, w, b, r, act="gelu") for _ in range(3)]
     side.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("M,N,K,layout,gated,plan", cases.PRODUCTS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_every_body(dense, M, N, K, layout, gated, plan, dtype):
+    act = "silu" if gated else ("gelu" if M % 2 else "gelu_tanh")
+    check(dense, M, N, K, act, gated, layout, dtype, True, True, train=False)
+
+
+@pytest.mark.parametrize("M,N,K,plan", cases.GRADIENTS)
+@pytest.mark.parametrize("layout,dtype", [("nk", "f16"), ("kn", "bf16")])
+def test_every_body_of_the_weight_gradient(dense, M, N, K, plan, layout, dtype):
+    print(M, N, K, layout, dtype, flush=True)
+    if layout == "kn":  # dw is [K, N] there: the same tiles
+        N, K = K, N
+    x, w, _, _, dy = inputs(M, N, K, False, layout, dtype)
+    _, dw, _ = dense.matmul_backward(dy, x, w, layout=layout, need_dx=False)
+    refs.check_backward(None, dw, None, dy, x, w, None, "none", False, layout)
+
+
+@pytest.mark.parametrize("N,K", [(1, 1), (1, 64), (2, 9), (3, 200), (4, 40), (7, 7), (9, 3)])
+@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_narrow_matrices(dense, M, N, K, gated, layout):
+    check(dense, M, N, K, "gelu", gated, layout, "f16", True, True)
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_infinities_and_nan_stay_in_their_rows(dense, M):
+    x, w, b, r, dy = inputs(M, 72, 64, True, "nk", "bf16")
+    want, zw = dense.matmul(x, w, b, r, act="silu", gated=True, preactivation=True)
+    dxw, _, _ = dense.matmul_backward(dy, x, w, zw, act="silu", gated=True, need_dw=False)
+    x2, dy2 = x.clone(), dy.clone()
+    x2[1, 5], dy2[2, 3] = float("inf"), float("nan")
+    y, z = dense.matmul(x2, w, b, r, act="silu", gated=True, preactivation=True)
+    dx, _, _ = dense.matmul_backward(dy2, x, w, zw, act="silu", gated=True, need_dw=False)
+    other = [i for i in range(M) if i != 1]
+    assert not bool(y[1].isfinite().all()) and torch.equal(y[other], want[other]) and torch.equal(z[other], zw[other])
+    other = [i for i in range(M) if i != 2]
+    assert bool(dx[2].isnan().all()) and torch.equal(dx[other], dxw[other])
+
+
+def test_large_gradients_are_read_past_the_cache(dense):
+    """The activation's gradient of more bytes than the memory-side cache holds."""
+    check(dense, 8200, 7176, 24, "gelu", False, "nk", "bf16", True, False)
+
+
+def test_a_layer_feeds_a_router_and_the_experts(dense):
+    """Training through the linear layer, the router and the routed operators: each node's gradient is its operator's own."""
+    from persistent_tile_scheduling_macro_amd import moe
+    T, H, I, E, k = 96, 128, 72, 6, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def normal(*shape, scale=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * scale).bfloat16().requires_grad_(True)
+
+    x, w_x, router = normal(T, H), normal(2 * H, H, scale=H ** -0.5), normal(E, H, scale=H ** -0.5)
+    w_in, w_out = normal(E, I, H, scale=H ** -0.5), normal(E, H, I, scale=I ** -0.5)
+    leaves = (x, w_x, router, w_in, w_out)
+    dout = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+
+    def step():
+        h = dense.matmul(x, w_x, None, x, act="silu", gated=True)
+        ids, weights = moe.route(dense.matmul(h, router), k)
+        rows, plan = moe.dispatch(h, ids, E)
+        out = moe.combine(moe.grouped_matmul(moe.grouped_matmul(rows, w_in, plan.offsets), w_out, plan.offsets), weights, plan)
+        return (out.detach(),) + torch.autograd.grad(out, leaves, dout)
+
+    def by_hand():
+        with torch.no_grad():
+            h, z = dense.matmul(x, w_x, None, x, act="silu", gated=True, preactivation=True)
+            logits = dense.matmul(h, router)
+            ids, weights = moe.route(logits, k)
+            rows, plan = moe.dispatch(h, ids, E)
+            up = moe.grouped_matmul(rows, w_in, plan.offsets)
+            down = moe.grouped_matmul(up, w_out, plan.offsets)
+            out = moe.combine(down, weights, plan)
+            ddown, dweights = moe.combine_backward(dout, down, weights, plan)
+            dup, dw_out = moe.grouped_matmul_backward(ddown, up, w_out, plan.offsets)
+            drows, dw_in = moe.grouped_matmul_backward(dup, rows, w_in, plan.offsets)
+            dlogits = moe.route_backward(dweights, logits, ids, weights)
+            dh1, drouter, _ = dense.matmul_backward(dlogits, h, router)
+            dh2 = moe.dispatch_backward(drows, plan)
+            dh = dh1 + dh2
+            dx, dw_x, _ = dense.matmul_backward(dh, x, w_x, z, act="silu", gated=True)
+            return out, dx + dh, dw_x, drouter, dw_in, dw_out
+
+    want = by_hand()
+    for a, b in zip(step(), want):
+        assert torch.equal(a, b) or (a.double() - b.double()).norm() <= 2.0 ** -7 * b.double().norm()  # sums of two in either order
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.copy_(torch.randn((T, H), generator=g, device="cuda").bfloat16())
+        eager = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, eager):
+            assert torch.equal(a, b)
