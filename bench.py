@@ -148,14 +148,15 @@ def source_digest() -> str:
     """sha256 over the code (comments and blank space removed) that decides what the
     GEMM's launches move: its kernels and the launch planner. HBM counters are only
     reported for the code they came from. Left out are the host's declarations of the
-    handle and of the launch call, and the sources of the routed operators and the
-    4-bit product, which the timed workloads do not run."""
+    handle and of the launch call, and the sources of the routed operators, the 4-bit
+    product and the linear layer, which the timed workloads do not run."""
     import hashlib
     import re
 
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".h", ".hip")) and not name.startswith(("moe", "grouped", "w4", "context.h", "launch.h")):
+        if name.endswith((".h", ".hip")) and not name.startswith(("moe", "grouped", "w4", "dense", "route", "layer", "context.h",
+                                                                              "launch.h")):
             with open(os.path.join(CSRC, name), encoding="utf-8") as f:
                 text = f.read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)

@@ -2,9 +2,10 @@
 
     python examples/moe_layer.py
 
-Training: the router's choices send each token's row to its experts (moe.dispatch), two grouped products with a gated
-activation between them, and the rows come back weighted (moe.combine); gradients run through the same operators.
-Decoding: the trained matrices, as int4 codes with a scale for every 64 elements, multiply a few rows (w4.matmul).
+Training: the router (moe.route) chooses each token's experts, its row goes there (moe.dispatch), two grouped products
+with a gated activation between them, and the rows come back weighted (moe.combine); gradients run through the same
+operators. Decoding: a few tokens through the whole layer in two launches (moe.layer), and the same with the trained
+matrices as int4 codes with a scale for every 64 elements (w4.matmul).
 """
 import os
 import sys
@@ -20,8 +21,7 @@ GROUP = 64
 
 def route(x, router, k):
     """Each token's k experts and their weights, which sum to one."""
-    weights, ids = torch.topk(torch.softmax(x.float() @ router, dim=1), k, dim=1)
-    return ids, weights / weights.sum(1, keepdim=True)
+    return moe.route(x.float() @ router, k)
 
 
 def layer(x, router, w_in, w_out, k, product):
@@ -65,7 +65,7 @@ def run(T=512, H=256, W=384, E=8, k=2, steps=3, device="cuda:0"):
 
     with torch.no_grad():
         few = x[:4]
-        want = layer(few, router, w_in, w_out, k, lambda r, w, o: moe.grouped_matmul(r, w, o, layout="nk"))
+        want = moe.layer(few, *route(few, router, k), w_in, w_out)
         packed = {id(w): quantize(w) for w in (w_in, w_out)}
         got = layer(few, router, w_in, w_out, k,
                     lambda r, w, o: w4.matmul(r, *packed[id(w)], group=GROUP, offsets=o))
