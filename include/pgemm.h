@@ -625,6 +625,11 @@ int pgemm_dense_query(int64_t M, int64_t N, int64_t K, int layout, int gated, in
 /* The same for the gradient of W: [I, J] = a^T b over R rows. */
 int pgemm_dense_weight_grad_query(int64_t R, int64_t I, int64_t J, int* body, int* pieces);
 
+/* Whether the gradients of x and W, both asked for, go into one launch: its body
+ * and each one's pieces (which each keeps where it alone is asked for, so that
+ * its values stay the same); a body of -1 for two, as the queries above tell them. */
+int pgemm_dense_gradients_query(int64_t M, int64_t C, int64_t K, int layout, int* body, int* pieces_dx, int* pieces_dw);
+
 /* ---- the router, and a routed layer of few tokens ----------------------- */
 
 /* Type of the router's logits. */

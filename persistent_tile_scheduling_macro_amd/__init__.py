@@ -168,6 +168,7 @@ _dense_backward_workspace = _sig("pgemm_dense_backward_workspace", _int, _i64, _
                                  ctypes.POINTER(_i64))
 _dense_query = _sig("pgemm_dense_query", _int, _i64, _i64, _i64, _int, _int, _ip, _ip)
 _dense_weight_grad_query = _sig("pgemm_dense_weight_grad_query", _int, _i64, _i64, _i64, _ip, _ip)
+_dense_gradients_query = _sig("pgemm_dense_gradients_query", _int, _i64, _i64, _i64, _int, _ip, _ip, _ip)
 _moe_route = _sig("pgemm_moe_route", _int, _vp, _vp, _i64, _int, _i64, _i64, _i64, _int, _int, _vp, _vp)
 _moe_route_backward = _sig("pgemm_moe_route_backward", _int, _vp, _vp, _vp, _i64, _int, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp)
 _moe_layer = _sig("pgemm_moe_layer", _int, _vp, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _int,
@@ -386,6 +387,13 @@ def pgemm_dense_weight_grad_query(R: int, I: int, J: int) -> tuple:
     body, pieces = ctypes.c_int(), ctypes.c_int()
     _check(_dense_weight_grad_query(R, I, J, ctypes.byref(body), ctypes.byref(pieces)))
     return body.value, pieces.value
+
+
+def pgemm_dense_gradients_query(M: int, C: int, K: int, layout: int) -> tuple:
+    """(PGEMM_DENSE_* body, pieces of dx, pieces of dw) of the launch that computes both gradients, -1 for two launches."""
+    body, px, pw = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    _check(_dense_gradients_query(M, C, K, layout, ctypes.byref(body), ctypes.byref(px), ctypes.byref(pw)))
+    return body.value, px.value, pw.value
 
 
 def pgemm_moe_route(h, logits, ld: int, type: int, T: int, E: int, k: int, score: int, normalize: int, ids, weights) -> None:

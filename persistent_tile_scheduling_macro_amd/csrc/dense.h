@@ -205,6 +205,8 @@ struct SideArgs {
 struct Kernels {
   kernel_fn (*pick)(int body, int form, bool gated);
   kernel_fn join[2]; // by gated
+  void (*(*pick_both)(int body, int form))(Args, Args, int, int);
+  void (*join_both)(Args, Args, int);
   void (*act_grad[2])(ActGradArgs);
   void (*side)(SideArgs);
 };

@@ -34,7 +34,7 @@ static_assert((int)act::kNone == (int)PGEMM_ACT_NONE && (int)act::kRelu == (int)
                   (int)act::kGeluTanh == (int)PGEMM_ACT_GELU_TANH && (int)act::kSilu == (int)PGEMM_ACT_SILU,
               "the header's numbers are the activations'");
 
-struct Plan { int body; int split; };
+struct Plan { int body; int split; double time; };
 
 struct Tile { int bm, bn; };
 Tile tile_of(int body) { return body == dense::kPing ? Tile{256, 256} : body == dense::kTile64 ? Tile{64, 128} : Tile{128, 128}; }
@@ -87,14 +87,14 @@ double tile_time(int body, int64_t rows, int64_t columns, int64_t sum, int64_t p
 }
 
 // Tries a tile body with the numbers of pieces that leave each at least two steps of 64.
-void try_tiles(int body, int64_t rows, int64_t columns, int64_t sum, double extra, Plan* best, double* least) {
+void try_tiles(int body, int64_t rows, int64_t columns, int64_t sum, double extra, Plan* best) {
   const int64_t steps = ceil_div(sum, 64);
   for (int pieces : {1, 2, 3, 4, 6, 8, 12}) {
     if (pieces > 1 && (pieces * 2 > steps || (body == dense::kTile128Pair && pieces > 4))) break;
     const Tile t = tile_of(body);
     if (pieces > 1 && ceil_div(rows, t.bm) * ceil_div(columns, t.bn) * pieces > 1024) break;
     const double time = extra + tile_time(body, rows, columns, sum, pieces);
-    if (time < *least) *best = {body, pieces}, *least = time;
+    if (time < best->time) *best = {body, pieces, time};
   }
 }
 
@@ -102,18 +102,17 @@ void try_tiles(int body, int64_t rows, int64_t columns, int64_t sum, double extr
 // need moved first (a launch of 3 us and a pass over the operand).
 Plan plan_rows(int64_t M, int64_t N, int64_t K, bool nk, bool gated, bool pad_x, bool pad_w) {
   const int64_t C = gated ? 2 * N : N;
-  Plan best = {dense::kTile128, 1};
-  double least = 1e30;
+  Plan best = {dense::kTile128, 1, 1e30};
   const double extra = pad_x * (3 + 1e-6 * M * K) + pad_w * (3 + 1e-6 * C * K);
-  if (N % 8 == 0) try_tiles(dense::kPing, M, C, K, extra, &best, &least);
-  try_tiles(dense::kTile128, M, C, K, extra, &best, &least);
-  try_tiles(dense::kTile128Pair, M, C, K, extra, &best, &least);
-  if (M <= 512) try_tiles(dense::kTile64, M, C, K, extra, &best, &least);
+  if (N % 8 == 0) try_tiles(dense::kPing, M, C, K, extra, &best);
+  try_tiles(dense::kTile128, M, C, K, extra, &best);
+  try_tiles(dense::kTile128Pair, M, C, K, extra, &best);
+  if (M <= 512) try_tiles(dense::kTile64, M, C, K, extra, &best);
   if (M <= 128 && (nk || N >= 4)) {
     for (int body : {(int)dense::kFew8, (int)dense::kFew16, (int)dense::kFew32}) {
       if (M > 16 ? body == dense::kFew8 : few_rows(body) / 2 >= M && body > dense::kFew8) continue;
       const double time = few_time(body, M, N, K, nk, gated);
-      if (time < least) best = {body, 1}, least = time;
+      if (time < best.time) best = {body, 1, time};
     }
   }
   return best;
@@ -121,12 +120,66 @@ Plan plan_rows(int64_t M, int64_t N, int64_t K, bool nk, bool gated, bool pad_x,
 
 // The same for c [I][J] = a^T b over R rows.
 Plan plan_grad(int64_t R, int64_t I, int64_t J) {
-  Plan best = {dense::kTile128, 1};
-  double least = 1e30;
-  if (J % 8 == 0) try_tiles(dense::kPing, I, J, R, 0, &best, &least);
-  try_tiles(dense::kTile128, I, J, R, 0, &best, &least);
-  try_tiles(dense::kTile128Pair, I, J, R, 0, &best, &least);
+  Plan best = {dense::kTile128, 1, 1e30};
+  if (J % 8 == 0) try_tiles(dense::kPing, I, J, R, 0, &best);
+  try_tiles(dense::kTile128, I, J, R, 0, &best);
+  try_tiles(dense::kTile128Pair, I, J, R, 0, &best);
   return best;
+}
+
+// Both products of a backward pass, dx [M][K] over C and dw over M, as tiles of 128 x 128 in one launch, if that is faster
+// than one after the other. The workgroups are laid on the card's slots as the hardware does, the longer ones first.
+struct Both { int body, split_x, split_w; bool dw_first; };
+bool plan_both(int64_t M, int64_t K, int64_t C, bool nk, const Plan& dx, const Plan& dw, Both* best) {
+  if (dx.body <= dense::kFew32) return false;
+  const int64_t I = nk ? C : K, J = nk ? K : C;
+  const int64_t steps_x = ceil_div(C, 64), steps_w = ceil_div(M, 64);
+  const int64_t tiles_x = ceil_div(M, 128) * ceil_div(K, 128), tiles_w = ceil_div(I, 128) * ceil_div(J, 128);
+  if (tiles_x + tiles_w > 1024) return false; // each fills the card by itself
+  double least = dx.time + dw.time;
+  bool found = false;
+  for (int body : {(int)dense::kTile128, (int)dense::kTile128Pair}) {
+    const TileCost& c = kTileCost[body - dense::kTile64];
+    const int64_t slots = body == dense::kTile128Pair ? 512 : 256;
+    for (int px : {1, 2, 3, 4, 6, 8, 12}) {
+      if (px > 1 && (px * 2 > steps_x || tiles_x * px > 1024 || (slots == 512 && px > 4))) break;
+      for (int pw : {1, 2, 3, 4, 6, 8, 12}) {
+        if (pw > 1 && (pw * 2 > steps_w || tiles_w * pw > 1024 || (slots == 512 && pw > 4))) break;
+        const int64_t groups_x = tiles_x * px, groups_w = tiles_w * pw;
+        if ((px > 1 || pw > 1) && groups_x + groups_w > 2 * slots) break; // pieces are for few tiles
+        double load = (groups_x + groups_w) / 256.0 - (slots == 512);
+        load = load < 0 ? 0 : load > 1 ? 1 : load;
+        const double step = c.step + (c.full - c.step) * load;
+        const double time_x = c.start + (double)steps_x / px * step, time_w = c.start + (double)steps_w / pw * step;
+        const bool dw_first = time_w > time_x;
+        const int64_t first = dw_first ? groups_w : groups_x, then = dw_first ? groups_x : groups_w;
+        const double longer = dw_first ? time_w : time_x, shorter = dw_first ? time_x : time_w;
+        // after the first: `late` slots are busy a round longer than the others
+        const int64_t late = first % slots;
+        double early_end = (double)(first / slots) * longer, late_end = late ? early_end + longer : early_end;
+        double end = late_end;
+        for (int64_t left = then; left > 0;) {
+          const bool take_late = late && late_end < early_end;
+          double& at = take_late ? late_end : early_end;
+          at += shorter;
+          end = at > end ? at : end;
+          left -= take_late ? late : slots - late;
+        }
+        const double elements_x = (double)M * K, elements_w = (double)I * J;
+        const double reads = 2.0 * (2 * (double)M * C + 2 * elements_w + 2 * elements_x) / 5e6;
+        double time = c.base + (end > reads ? end : reads);
+        if (px > 1 || pw > 1)
+          time += c.join + 0.15 * (px > pw ? px : pw) + c.join_sum * 1e-6 * ((px > 1 ? px * elements_x : 0) + (pw > 1 ? pw * elements_w : 0));
+        if (time < least) *best = {body, px, pw, dw_first}, least = time, found = true;
+      }
+    }
+  }
+  return found;
+}
+// One of them by itself: 128 x 128 tiles with as many pieces (all such bodies add a piece's products in the same order).
+Plan one_of(int64_t rows, int64_t columns, int64_t sum, int pieces) {
+  const double one = tile_time(dense::kTile128, rows, columns, sum, pieces), two = tile_time(dense::kTile128Pair, rows, columns, sum, pieces);
+  return {one < two ? (int)dense::kTile128 : (int)dense::kTile128Pair, pieces, one < two ? one : two};
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
@@ -169,10 +222,28 @@ struct Call {
     launch((int64_t)side.pad_blocks[0] + side.pad_blocks[1] + (side.C + 63) / 64, 256, kernels.side, side);
   }
 
+  // The pieces' sums, and the tiles.
+  void lay_out(Args& a, int body, int pieces, bool gated) {
+    a.split = pieces;
+    if (pieces > 1) a.part = scratch.take<float>(pieces * (int64_t)a.M * dense::part_ld(a, gated));
+    const Tile t = tile_of(body);
+    a.n_m = (int)((a.M + t.bm - 1) / t.bm);
+    a.n_n = (int)(((gated ? 2 * (int64_t)a.N : a.N) + t.bn - 1) / t.bn);
+  }
+  static int64_t tile_groups(const Args& a) { return ((int64_t)a.n_m * a.n_n * a.split + 7) / 8 * 8; }
+  static int64_t join_groups(const Args& a) { return a.split > 1 ? ((int64_t)a.M * ((a.N + 7) / 8) + 255) / 256 : 0; }
+
+  void both(Args dx, Args dw, const Both& plan, int form) {
+    lay_out(dx, plan.body, plan.split_x, false);
+    lay_out(dw, plan.body, plan.split_w, false);
+    if (!h) return;
+    launch(tile_groups(dx) + tile_groups(dw), 512, kernels.pick_both(plan.body, form), dx, dw,
+           (int)tile_groups(plan.dw_first ? dw : dx), (int)plan.dw_first);
+    launch(join_groups(dx) + join_groups(dw), 256, kernels.join_both, dx, dw, (int)join_groups(dx));
+  }
+
   void product(Args a, Plan plan, int form, bool gated) {
-    const int64_t columns = gated ? 2 * (int64_t)a.N : a.N;
-    a.split = plan.split;
-    if (plan.split > 1) a.part = scratch.take<float>(plan.split * (int64_t)a.M * dense::part_ld(a, gated));
+    lay_out(a, plan.body, plan.split, gated);
     if (!h) return;
     const dense::kernel_fn kernel = kernels.pick(plan.body, form, gated);
     if (plan.body <= dense::kFew32) {
@@ -181,14 +252,9 @@ struct Call {
         status = enqueue(h->stream, dim3((unsigned)((a.N + wide - 1) / wide), (unsigned)((a.M + rows - 1) / rows)), dim3(512), kernel, a);
       return;
     }
-    const Tile t = tile_of(plan.body);
-    a.n_m = (int)((a.M + t.bm - 1) / t.bm);
-    a.n_n = (int)((columns + t.bn - 1) / t.bn);
     const int64_t total = (int64_t)a.n_m * a.n_n * a.split;
-    if (plan.body == dense::kPing) launch(total < h->cus ? total : h->cus, 512, kernel, a);
-    else launch((total + 7) / 8 * 8, 512, kernel, a);
-    if (plan.split > 1)
-      launch(((int64_t)a.M * ((a.N + 7) / 8) + 255) / 256, 256, kernels.join[gated], a);
+    launch(plan.body != dense::kPing ? tile_groups(a) : total < h->cus ? total : h->cus, 512, kernel, a);
+    launch(join_groups(a), 256, kernels.join[gated], a);
   }
 };
 
@@ -285,37 +351,39 @@ void backward(Call& c, const Gradients& g) {
   }
   // dx = dz [M, C] times W, the sum running over W's columns; dW = x^T dz or its transpose
   const int form = nk ? dense::kRowsKN : dense::kRowsNK;
-  const Plan plan = plan_rows(g.M, g.K, C, !nk, false, false, (nk ? g.K : C) % 8);
+  Plan plan = plan_rows(g.M, g.K, C, !nk, false, false, (nk ? g.K : C) % 8);
   Operand w = {static_cast<const uint16_t*>(g.w), g.ldw}, x = {static_cast<const uint16_t*>(g.x), g.ldx};
   if (products && g.need_dx && plan.body > dense::kFew32)
     w = nk ? c.operand(g.w, g.ldw, C, g.K, 1, g.wide_w) : c.operand(g.w, g.ldw, g.K, C, 1, g.wide_w);
   if (products && g.need_dw) x = c.operand(g.x, g.ldx, g.M, g.K, 1, g.wide_x);
   c.prepare();
   if (!products) return;
-  if (g.need_dx) {
-    Args a = {};
-    a.a = dz.p;
-    a.lda = dz.ld;
-    a.b = w.p;
-    a.ldb = w.ld;
-    a.c = static_cast<uint16_t*>(g.dx);
-    a.M = (int)g.M;
-    a.N = (int)g.K;
-    a.K = (int)C;
-    c.product(a, plan, form, false);
+  Args dx = {}, dw = {};
+  dx.a = dz.p;
+  dx.lda = dz.ld;
+  dx.b = w.p;
+  dx.ldb = w.ld;
+  dx.c = static_cast<uint16_t*>(g.dx);
+  dx.M = (int)g.M;
+  dx.N = (int)g.K;
+  dx.K = (int)C;
+  dw.a = nk ? dz.p : x.p;
+  dw.lda = nk ? dz.ld : x.ld;
+  dw.b = nk ? x.p : dz.p;
+  dw.ldb = nk ? x.ld : dz.ld;
+  dw.c = static_cast<uint16_t*>(g.dw);
+  dw.M = (int)(nk ? C : g.K);
+  dw.N = (int)(nk ? g.K : C);
+  dw.K = (int)g.M;
+  Plan dw_plan = plan_grad(g.M, dw.M, dw.N);
+  Both both;
+  if (plan_both(g.M, g.K, C, nk, plan, dw_plan, &both)) {
+    if (g.need_dx && g.need_dw) return c.both(dx, dw, both, form);
+    plan = one_of(g.M, g.K, C, both.split_x); // the same sums, to the bit, where one of them is wanted
+    dw_plan = one_of(dw.M, dw.N, g.M, both.split_w);
   }
-  if (g.need_dw) {
-    Args a = {};
-    a.a = nk ? dz.p : x.p;
-    a.lda = nk ? dz.ld : x.ld;
-    a.b = nk ? x.p : dz.p;
-    a.ldb = nk ? x.ld : dz.ld;
-    a.c = static_cast<uint16_t*>(g.dw);
-    a.M = (int)(nk ? C : g.K);
-    a.N = (int)(nk ? g.K : C);
-    a.K = (int)g.M;
-    c.product(a, plan_grad(g.M, a.M, a.N), dense::kGrad, false);
-  }
+  if (g.need_dx) c.product(dx, plan, form, false);
+  if (g.need_dw) c.product(dw, dw_plan, dense::kGrad, false);
 }
 
 int short_of(pgemm_ctx* h, int64_t need, const void* work, int64_t have) {
@@ -456,6 +524,20 @@ int pgemm_dense_weight_grad_query(int64_t R, int64_t I, int64_t J, int* body, in
   const Plan p = plan_grad(R, I, J);
   *body = p.body;
   *pieces = p.split;
+  return PGEMM_OK;
+}
+
+int pgemm_dense_gradients_query(int64_t M, int64_t C, int64_t K, int layout, int* body, int* pieces_dx, int* pieces_dw) {
+  if (!body || !pieces_dx || !pieces_dw || M < 1 || C < 1 || K < 1) return PGEMM_ERR_INVALID_ARG;
+  const int rc = check(nullptr, M, C, K, layout, 0, 0, PGEMM_F16);
+  if (rc != PGEMM_OK) return rc;
+  const bool nk = layout == PGEMM_B_NK;
+  const Plan dx = plan_rows(M, K, C, !nk, false, false, (nk ? K : C) % 8), dw = plan_grad(M, nk ? C : K, nk ? K : C);
+  Both both;
+  const bool one = plan_both(M, K, C, nk, dx, dw, &both);
+  *body = one ? both.body : -1;
+  *pieces_dx = one ? both.split_x : dx.split;
+  *pieces_dw = one ? both.split_w : dw.split;
   return PGEMM_OK;
 }
 

@@ -31,8 +31,14 @@ kernel_fn pick(int body, int form, bool gated) {
   return gated ? pick_form<DT, kRowsKN, true>(body) : pick_form<DT, kRowsKN, false>(body);
 }
 template <int DT>
+void (*pick_both(int body, int form))(Args, Args, int, int) {
+  const bool pair = body == kTile128Pair;
+  if (form == kRowsNK) return pair ? both_kernel<DT, kRowsNK, 2> : both_kernel<DT, kRowsNK, 4>;
+  return pair ? both_kernel<DT, kRowsKN, 2> : both_kernel<DT, kRowsKN, 4>;
+}
+template <int DT>
 Kernels kernels() {
-  return {pick<DT>, {join_kernel<DT, false>, join_kernel<DT, true>},
+  return {pick<DT>, {join_kernel<DT, false>, join_kernel<DT, true>}, pick_both<DT>, join_both_kernel<DT>,
           {act_grad_kernel<DT, false>, act_grad_kernel<DT, true>}, side_kernel<DT>};
 }
 

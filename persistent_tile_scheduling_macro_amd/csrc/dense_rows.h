@@ -9,9 +9,9 @@ namespace dense {
 
 // c = epilogue(sum of the pieces' sums), eight columns a thread, pieces in order.
 template <int DT, bool GATED>
-__global__ void __launch_bounds__(256) join_kernel(Args a) {
+__device__ inline void join_pieces(const Args& a, int block) {
   const int chunks = (a.N + 7) / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / chunks;
+  const int64_t i = (int64_t)block * 256 + threadIdx.x, m = i / chunks;
   if (m >= a.M) return;
   const int n = (int)(i - m * chunks) * 8;
   const int64_t ld = part_ld(a, GATED), stride = a.M * ld;
@@ -41,6 +41,16 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
   act::with_path(epilogue.k, [&](auto path) __attribute__((always_inline)) {
     epilogue.template finish<decltype(path)::value>((int)m, n, v, u, bv, bu);
   });
+}
+template <int DT, bool GATED>
+__global__ void __launch_bounds__(256) join_kernel(Args a) {
+  join_pieces<DT, GATED>(a, blockIdx.x);
+}
+// Of two products, the first one in `head` workgroups.
+template <int DT>
+__global__ void __launch_bounds__(256) join_both_kernel(Args a, Args b, int head) {
+  if ((int)blockIdx.x < head) join_pieces<DT, false>(a, blockIdx.x);
+  else join_pieces<DT, false>(b, blockIdx.x - head);
 }
 
 // dz and the column sums of it. A workgroup takes 512 columns of y (a wave's

@@ -28,8 +28,11 @@ using fast::read_b;
 using fast::static_for;
 using fast::wait_vmcnt;
 
+constexpr int ring_bytes(int rows, int stages) { return stages * (rows + 128) * 128; }
+
+// The tile of workgroup `block` of a's grid, with `ring` its LDS.
 template <int DT, int FORM, bool GATED, int BM, int S>
-__global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
+__device__ __attribute__((always_inline)) inline void run_tile(const Args& a, int block, uint8_t* ring) {
   constexpr int BN = 128, BK = 64;
   constexpr bool A_KC = FORM != kGrad, B_KC = FORM == kRowsNK;
   static_assert(A_KC || BM == 128, "the transposed rows of A are 256 bytes in LDS");
@@ -38,7 +41,7 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
   constexpr int ROW_OC = 256;
   typedef typename fast::Frag<DT>::t frag_t;
   constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128; // A's tile, then B's
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
+  static_assert(S * STAGE == ring_bytes(BM, S), "the ring is its stages");
   auto stage_a = [&](auto c) __attribute__((always_inline)) -> uint8_t* { return ring + decltype(c)::value * STAGE; };
   auto stage_b = [&](auto c) __attribute__((always_inline)) -> uint8_t* { return stage_a(c) + A_BYTES; };
 
@@ -49,8 +52,8 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
 
   // tiles of one piece follow each other; each XCD takes one stretch of the sequence
   const int per = a.n_m * a.n_n, total = per * a.split, share = (total + 7) / 8;
-  const int u = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= share || u >= total) return;
+  const int u = (block & 7) * share + (block >> 3);
+  if ((block >> 3) >= share || u >= total) return;
   const int piece = u / per;
   int pm, pn, first, nk;
   grouped_tile(u - piece * per, a.n_m, a.n_n, 8, &pm, &pn);
@@ -255,6 +258,25 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
       }
     }
   }
+}
+
+template <int DT, int FORM, bool GATED, int BM, int S>
+__global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(BM, S)];
+  run_tile<DT, FORM, GATED, BM, S>(a, blockIdx.x, ring);
+}
+
+// Both products of a backward pass in one launch, dx in form FORM: their tiles fill the card together, which the tiles
+// of one alone often do not (forward and backward of 4477 x 1552 x 1988: 156 us, in two launches 179; 802 x 1400 x 96: 27 and
+35 us; 4099 x 2057 x 1021: 145 and 153). The first `head` workgroups (a multiple of 8) have the longer sums. Four stages
+rather than five: the unrolled steps of both products then fit the scalar registers.
+template <int DT, int FORM, int S>
+__global__ void __launch_bounds__(512, S == 2 ? 4 : 2) both_kernel(Args dx, Args dw, int head, int dw_first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(128, S)];
+  const bool first = (int)blockIdx.x < head;
+  const int block = first ? blockIdx.x : blockIdx.x - head;
+  if (first == (dw_first != 0)) run_tile<DT, kGrad, false, 128, S>(dw, block, ring);
+  else run_tile<DT, FORM, false, 128, S>(dx, block, ring);
 }
 
 } // namespace dense

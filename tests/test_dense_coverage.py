@@ -49,3 +49,15 @@ def test_few_columns_of_k_by_n_weights_leave_the_few_row_body():
     for N in (1, 2, 3):
         assert pg.pgemm_dense_query(4, N, 64, LAYOUT["kn"])[0] not in FEW
         assert pg.pgemm_dense_query(4, N, 64, LAYOUT["nk"])[0] in FEW
+
+
+@pytest.mark.parametrize("M,N,K,layout,plan", cases.BOTH)
+def test_both_gradients_take_the_launch_they_name(M, N, K, layout, plan):
+    assert pg.pgemm_dense_gradients_query(M, N, K, LAYOUT[layout]) == plan
+
+
+def test_every_launch_of_both_gradients_is_reached():
+    got = {(layout, body, dx > 1, dw > 1) for _, _, _, layout, (body, dx, dw) in cases.BOTH}
+    assert {(layout, body) for layout, body, _, _ in got} == {(l, b) for l in LAYOUT for b in (cases.TILE128, cases.PAIR, cases.TWO)}
+    assert {(dx, dw) for _, body, dx, dw in got if body != cases.TWO} == {(a, b) for a in (False, True) for b in (False, True)}
+    assert any(N % 8 for _, N, _, _, (b, *_) in cases.BOTH if b != cases.TWO) and any(K % 8 for _, _, K, _, (b, *_) in cases.BOTH if b != cases.TWO)

@@ -235,6 +235,16 @@ def test_every_body_of_the_weight_gradient(dense, M, N, K, plan, layout, dtype):
     refs.check_backward(None, dw, None, dy, x, w, None, "none", False, layout)
 
 
+@pytest.mark.parametrize("M,N,K,layout,plan", cases.BOTH)
+@pytest.mark.parametrize("act,dtype", [("none", "f16"), ("silu", "bf16")])
+def test_both_gradients(dense, M, N, K, layout, plan, act, dtype):
+    print(M, N, K, layout, act, dtype, flush=True)
+    x, w, b, _, dy = inputs(M, N, K, False, layout, dtype)
+    _, z = dense.matmul(x, w, b, act=act, layout=layout, preactivation=True)
+    dx, dw, db = dense.matmul_backward(dy, x, w, z, act=act, layout=layout, need_dbias=True)
+    refs.check_backward(dx, dw, db, dy, x, w, z, act, False, layout)
+
+
 @pytest.mark.parametrize("N,K", [(1, 1), (1, 64), (2, 9), (3, 200), (4, 40), (7, 7), (9, 3)])
 @pytest.mark.parametrize("M", [1, 20, 200])
 @pytest.mark.parametrize("gated", [False, True])
