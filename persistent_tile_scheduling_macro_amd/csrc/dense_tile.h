@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) tile_kernel(Args a) {
 
 // Both products of a backward pass in one launch, dx in form FORM: their tiles fill the card together, which the tiles
 // of one alone often do not (forward and backward of 4477 x 1552 x 1988: 156 us, in two launches 179; 802 x 1400 x 96: 27 and
-35 us; 4099 x 2057 x 1021: 145 and 153). The first `head` workgroups (a multiple of 8) have the longer sums. Four stages
-rather than five: the unrolled steps of both products then fit the scalar registers.
+// 35 us; 4099 x 2057 x 1021: 145 and 153). The first `head` workgroups (a multiple of 8) have the longer sums. Four stages
+// rather than five: the unrolled steps of both products then fit the scalar registers.
 template <int DT, int FORM, int S>
 __global__ void __launch_bounds__(512, S == 2 ? 4 : 2) both_kernel(Args dx, Args dw, int head, int dw_first) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(128, S)];
