@@ -561,7 +561,7 @@ int pgemm_w4_query(int64_t M, int64_t N, int64_t E, int experts, int cus, int* r
  * gradient of z, too: it is an operand of the two products), the same on every
  * run. Sizes may be odd and addresses any that elements have; rows of a multiple
  * of 8 elements at 16-byte addresses are the fastest (others are moved to the
- * workspace first where M exceeds 32). `work` is device memory at a multiple of
+ * workspace first, but by the few-row bodies). `work` is device memory at a multiple of
  * 16, of at least the bytes that the workspace functions report, free again
  * once the call's work is done; nothing is allocated. Empty sums give the
  * epilogue of zero.

