@@ -55,27 +55,30 @@ __device__ inline float normal_cdf(float x, float* bell) {
   return x > 0.0f ? 1.0f - tail : tail;
 }
 
+// The square below 10^4, where every s is 0 or 1: silu's constant of 0 times it stays 0, and an x of +inf itself.
+__device__ inline float square(float x) { return __builtin_fminf(x * x, 1e4f); }
+
 template <int PATH>
 __device__ inline float value(float x, const Consts& c) {
   if constexpr (PATH == kCopy) {
     return x < c.floor ? 0.0f : x;
   } else if constexpr (PATH == kLogistic) {
-    return x * __builtin_amdgcn_rcpf(1.0f + exp2_fast(x * __builtin_fmaf(c.e1 * x, x, c.e0)));
+    return x * __builtin_amdgcn_rcpf(1.0f + exp2_fast(x * __builtin_fmaf(c.e1, square(x), c.e0)));
   } else {
     float bell;
     return x * normal_cdf(x, &bell);
   }
 }
 
-// Value and slope. (The backward pass over 8192 x 8192 pre-activations is bound by these instructions, not by their
-// bytes, so they are counted: the square is kept below 10^4, where every s is 0 or 1, instead of clamping x.)
+// Value and slope. (The backward pass takes as long for these instructions as for its bytes, so they are counted: an
+// infinite x has a slope of NaN, which clamping it would avoid.)
 template <int PATH>
 __device__ inline float value_and_slope(float x, const Consts& c, float* slope) {
   if constexpr (PATH == kCopy) {
     *slope = c.floor < 0.0f || x > 0.0f ? 1.0f : x != x ? x : 0.0f;
     return x < c.floor ? 0.0f : x;
   } else if constexpr (PATH == kLogistic) {
-    const float q = __builtin_fminf(x * x, 1e4f);
+    const float q = square(x);
     const float p = __builtin_amdgcn_rcpf(1.0f + exp2_fast(x * __builtin_fmaf(c.e1, q, c.e0)));
     const float value = x * p;
     *slope = __builtin_fmaf(value * (1.0f - p), __builtin_fmaf(3.0f * c.c1, q, c.c0), p);

@@ -268,6 +268,15 @@ def test_infinities_and_nan_stay_in_their_rows(dense, M):
     assert bool(dx[2].isnan().all()) and torch.equal(dx[other], dxw[other])
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [2, 200])
+def test_infinite_sums(dense, act, M):
+    x = torch.ones(M, 64, device="cuda", dtype=torch.bfloat16)
+    x[1, 3] = float("inf")
+    y = dense.matmul(x, torch.ones(80, 64, device="cuda", dtype=torch.bfloat16), act=act)
+    assert bool((y[1] == float("inf")).all()) and bool(y[0].isfinite().all())
+
+
 def test_large_gradients_are_read_past_the_cache(dense):
     """The activation's gradient of more bytes than the memory-side cache holds."""
     check(dense, 8200, 7176, 24, "gelu", False, "nk", "bf16", True, False)

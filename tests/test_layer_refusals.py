@@ -129,7 +129,8 @@ def test_workspaces():
 
 def test_queries_refuse():
     for call in (lambda: pg.pgemm_dense_query(0, 8, 8, 0), lambda: pg.pgemm_dense_query(8, 8, 8, 3),
-                 lambda: pg.pgemm_dense_weight_grad_query(8, 0, 8)):
+                 lambda: pg.pgemm_dense_weight_grad_query(8, 0, 8), lambda: pg.pgemm_dense_gradients_query(0, 8, 8, 0),
+                 lambda: pg.pgemm_dense_gradients_query(8, 8, 8, 2)):
         with pytest.raises(pg.PgemmError) as e:
             call()
         assert e.value.status == pg.PGEMM_ERR_INVALID_ARG
