@@ -343,3 +343,17 @@ def test_a_layer_feeds_a_router_and_the_experts(dense):
         torch.cuda.synchronize()
         for a, b in zip(captured, eager):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_offsets_past_32_bits(dense, gated):
+    """More than 2^31 elements of y, z and dz: their last rows and columns."""
+    M, N, K = 66001, 33000 // (1 + gated), 24
+    x, w, _, _, dy = inputs(M, N, K, gated, "nk", "bf16", False, False)
+    y, z = dense.matmul(x, w, act="silu", gated=gated, preactivation=True)
+    assert z.numel() > 2 ** 31
+    refs.check_forward(y[-70:], z[-70:], x[-70:], w, None, None, "silu", gated, "nk")
+    dx, dw, _ = dense.matmul_backward(dy, x, w, z, act="silu", gated=gated)
+    refs.check_backward(dx[-70:], None, None, dy[-70:], x[-70:], w, z[-70:], "silu", gated, "nk")
+    if not gated:
+        refs.check_backward(None, dw[-8:], None, dy[:, -8:], x, w[-8:], z[:, -8:], "silu", False, "nk")

@@ -168,3 +168,19 @@ def test_graph_capture(moe, T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, moe.layer(*a))
+
+
+def test_offsets_past_32_bits(moe):
+    """Matrices of more than 2^31 elements: the last experts."""
+    a = list(inputs(3, 2, 130, 4100, 2070, True, "bf16"))
+    a[3] = torch.cat([a[3], a[3][-4:]])  # with copies of the last ones
+    a[4] = torch.cat([a[4], a[4][-4:]])
+    assert a[3].numel() > 2 ** 31
+    a[1][:] = torch.tensor([[133, 0], [132, 131], [130, 133]], device="cuda")
+    check(moe.layer(*a), *a, "silu", True)
+
+
+def test_the_most_tokens(moe):
+    """4096 tokens go in 64 passes through one workspace."""
+    a = list(inputs(4096, 3, 9, 72, 40, True, "f16", drop=0.1))
+    check(moe.layer(*a), *a, "silu", True)
