@@ -564,8 +564,11 @@ int pgemm_w4_query(int64_t M, int64_t N, int64_t E, int experts, int cus, int* r
  * workspace first, but by the few-row bodies). `work` is device memory at a multiple of
  * 16, of at least the bytes that the workspace functions report, free again
  * once the call's work is done; nothing is allocated. Empty sums give the
- * epilogue of zero. An infinite z (an fp16 one beyond 65504 among them) has a
- * NaN gradient but for PGEMM_ACT_NONE and PGEMM_ACT_RELU.
+ * epilogue of zero. An fp16 z beyond 65504 is stored as that (y is formed from
+ * the fp32 sum all the same): without a gate its gradient is the true one, gated
+ * the other half's is that of 65504. An infinite sum stays infinite, and has a
+ * NaN gradient but for PGEMM_ACT_NONE and PGEMM_ACT_RELU. fp16 outputs, and dz,
+ * are infinite where they exceed 65504, and so are the sums that read such a dz.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size or
  * stride, an unknown layout, activation or type, or too small a workspace;
  * PGEMM_ERR_UNSUPPORTED for K or C above 2^21 or more tiles than one launch

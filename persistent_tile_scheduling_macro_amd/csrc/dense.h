@@ -62,6 +62,15 @@ __device__ inline u32x4 pack(const float* f) {
   return v;
 }
 
+// A pre-activation as the backward pass gets it. A finite one beyond fp16's range is stored as the type's largest value, not as
+// an infinity: past 100 every activation's slope is 1 or 0, so it keeps its gradient (as 0 times infinity that would be NaN, for
+// all of its row of dx and column of dW).
+template <int DT>
+__device__ inline float z_value(float v) {
+  if constexpr (DT == kF16) return __builtin_fabsf(v) < __builtin_huge_valf() ? __builtin_amdgcn_fmed3f(v, -65504.0f, 65504.0f) : v;
+  return v;
+}
+
 // Eight elements of a row, those past its end zeros.
 __device__ inline u32x4 load8_upto(const uint16_t* row, int64_t n, int64_t N) {
   return n + 8 <= N ? moe::load8<moe::kAnyAddress>(row + n) : moe::load_part(row + n, (int)(N - n));
@@ -83,6 +92,23 @@ struct Epilogue {
   __device__ inline void store(uint16_t* row, int n, const float* v) const {
     if constexpr (EVEN) moe::store8<moe::kAnyAddress>(row + n, pack<DT>(v));
     else moe::store_row<moe::kAnyAddress>(row, n, a.N, pack<DT>(v));
+  }
+
+  // One test for the eight costs nothing that can be measured (4096 x 4096 x 2048 gated: 123.6 us without any, 123.9 with it);
+  // putting each value right by itself costs 2%.
+  __device__ inline void store_z(uint16_t* row, int n, const float* v) const {
+    if constexpr (DT == kF16) {
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, __builtin_fabsf(v[i]));
+      if (__builtin_expect(__any(most > 65504.0f), 0)) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = z_value<DT>(v[i]);
+        return store(row, n, z);
+      }
+    }
+    store(row, n, v);
   }
 
   __device__ inline void bias_of(int n, float* bv, float* bu) const {
@@ -107,8 +133,8 @@ struct Epilogue {
     }
     if (a.z) {
       uint16_t* z = a.z + (int64_t)m * (GATED ? 2 * N : N);
-      store(z, n, v);
-      if constexpr (GATED) store(z + N, n, u);
+      store_z(z, n, v);
+      if constexpr (GATED) store_z(z + N, n, u);
     }
     u32x4 res = {0, 0, 0, 0};
     if (a.residual) res = load(a.residual + m * a.ldr, n);

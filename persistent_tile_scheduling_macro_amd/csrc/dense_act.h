@@ -71,7 +71,8 @@ __device__ inline float value(float x, const Consts& c) {
 }
 
 // Value and slope. (The backward pass takes as long for these instructions as for its bytes, so they are counted: an
-// infinite x has a slope of NaN, which clamping it would avoid.)
+// infinite x has a slope of NaN, which clamping it would avoid. It is that of an infinite sum alone: a finite one is stored
+// within its type's range.)
 template <int PATH>
 __device__ inline float value_and_slope(float x, const Consts& c, float* slope) {
   if constexpr (PATH == kCopy) {

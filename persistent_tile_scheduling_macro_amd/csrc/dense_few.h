@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(WAVES * 64, BLK == 8 ? 2 : 4) few_kernel(Args 
     const float up = u[r] + bias_up[r];
     if (a.z) {
       uint16_t* z = a.z + (int64_t)fm * (GATED ? 2 : 1) * N;
-      z[n] = bits(y);
-      if constexpr (GATED) z[N + n] = bits(up);
+      z[n] = bits(z_value<DT>(y));
+      if constexpr (GATED) z[N + n] = bits(z_value<DT>(up));
     }
     act::with_path(k, [&](auto path) __attribute__((always_inline)) { y = act::value<decltype(path)::value>(y, k); });
     if constexpr (GATED) y *= up;

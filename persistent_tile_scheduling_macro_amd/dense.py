@@ -41,8 +41,8 @@ def matmul(x, w, bias=None, residual=None, *, act: str = "none", gated: bool = F
 
     x [M, K]; w [C, K] (layout "nk") or [K, C] ("kn"); bias [C]; residual [M, N]; C = N, or 2N where gated, the gate's
     columns first. act is "none", "relu", "gelu" (with the error function), "gelu_tanh" or "silu". With
-    preactivation=True it returns (y, z), z [M, C] being what ``matmul_backward`` reads (None where it needs none), and
-    records no gradient itself.
+    preactivation=True it returns (y, z), z [M, C] being what ``matmul_backward`` reads (None where it needs none; an fp16 z
+    beyond 65504 is stored as that), and records no gradient itself.
     """
     act, nk = _act(act), _nk(layout)
     if preactivation:
