@@ -42,13 +42,17 @@ def matmul(x, w, bias=None, residual=None, *, act: str = "none", gated: bool = F
     x [M, K]; w [C, K] (layout "nk") or [K, C] ("kn"); bias [C]; residual [M, N]; C = N, or 2N where gated, the gate's
     columns first. act is "none", "relu", "gelu" (with the error function), "gelu_tanh" or "silu". With
     preactivation=True it returns (y, z), z [M, C] being what ``matmul_backward`` reads (None where it needs none; an fp16 z
-    beyond 65504 is stored as that), and records no gradient itself.
+    beyond 65504 is stored as that); it records no gradient, and refuses arguments that want one: call it under
+    ``torch.no_grad()`` or on detached tensors.
     """
     act, nk = _act(act), _nk(layout)
+    wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual))
     if preactivation:
-        with torch.no_grad():
-            return _ops.dense(x, w, bias, residual, act, gated, nk, True)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual)):
+        if wants:
+            raise ValueError("dense.matmul with preactivation=True records no gradient: call it under torch.no_grad() or on "
+                             "detached tensors")
+        return _ops.dense(x, w, bias, residual, act, gated, nk, True)
+    if wants:
         return _Dense.apply(x, w, bias, residual, act, gated, nk)
     return _ops.dense(x, w, bias, residual, act, gated, nk, False)[0]
 
