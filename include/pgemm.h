@@ -668,8 +668,12 @@ int pgemm_moe_route_backward(pgemm_handle_t h, const float* dweights, const void
  *   x: T rows of H, ldx apart; ids: [T, k] contiguous (outside [0, E): dropped;
  *   an expert named twice counts twice); weights: fp32 [T, k]; w_in: [E, I, H],
  *   gated [E, 2I, H]; w_out: [E, H, I]; out: [T, H].
- * Only the experts that a token names are read, once for each 64 tokens. Sums
- * are fp32 in a fixed order; a(x) and out are rounded once. `work` as for the
+ * Only the experts that a token names are read: once for each 16, 32 or 64 of
+ * the tokens that name one (the mean number of them decides which), so an expert
+ * that all of 64 tokens name is read up to four times. Sums are fp32 in an order
+ * that the ids of the pass's 64 tokens fix, so a token's last bits may depend on
+ * the ids of those beside it; a(x) and out are rounded once (an fp16 a(x) beyond
+ * 65504 is infinite, and so then is what it is summed into). `work` as for the
  * linear layer; nothing is allocated. dtype is PGEMM_F16 or PGEMM_BF16.
  * PGEMM_ERR_INVALID_ARG for a NULL handle or needed pointer, a negative size,
  * k < 1, E < 1, an unknown type or activation or too small a workspace;

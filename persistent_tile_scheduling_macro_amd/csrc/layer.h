@@ -2,11 +2,12 @@
 //   h[s] = act(x[t] W_in[e]^T)            gated: act(gate) * up of its 2I columns
 //   out[t] = sum over t's slots s of weights[s] * (h[s] W_out[e]^T)
 // with e = ids[s]. Reading the matrices of the experts that some token takes
-// bounds it; each is read once for up to 64 tokens.
+// bounds it; each is read once for every group of tokens that take it.
 //
-// A group is up to 16 MB of the tokens that take one expert (MB is chosen so that
-// nearly every expert is one group; another group reads the matrices again). A
-// token that names an expert twice is one row with the sum of its weights.
+// A group is up to 16 * MB of the tokens that take one expert. MB (1, 2 or 4) is
+// chosen by their mean number so that nearly every expert is one group; another
+// group reads the matrices again, four times in all at most. A token that names
+// an expert twice is one row with the sum of its weights.
 //
 // up_kernel: one workgroup for a group and 16 columns of h. It counts the tokens
 // of every expert from the ids and finds its group by a scan, so no sort and no
@@ -21,9 +22,11 @@
 // wave adds its sums, times the rows' weights, in fp32 to its own [T][16] part of
 // LDS; the waves' parts are added in order, and where several workgroups share
 // the columns, the last one to come adds all their parts in order. So no sum
-// depends on the order of atomics, no row of any expert's output goes through
-// memory, and h is the only intermediate value that is rounded (to 16 bits: it is
-// an MFMA operand; bf16 outputs are off by 0.0023 instead of one rounding's 0.0017).
+// depends on the order of atomics (but the ids of all tokens fix where the
+// groups' sums are cut: a token's last bits may depend on the others' ids), no
+// row of any expert's output goes through memory, and h is the only intermediate
+// value that is rounded (to 16 bits: it is an MFMA operand; bf16 outputs are off
+// by 0.0023 instead of one rounding's 0.0017).
 //
 // 32 tokens, 4 of 32 experts, 4096 x 2048 gated bf16: 182 and 117 us, 5.9 and 4.6
 // TB/s; one token, 8 of 64, 2048 x 1024 gated: 17 to 20 and 10 us, of each 3.9 the
