@@ -10,7 +10,8 @@ fp16 or bf16, sums and activations fp32, each output rounded once.
 ``matmul`` is differentiable in x, w, bias and residual; ``matmul_backward`` is its gradient as a function of its own,
 which is what to capture into a HIP graph. Errors are those of ``moe``: ValueError for shapes, TypeError for types,
 PgemmError for what the library refuses, NotImplementedError for a forward-mode tangent. A tensor whose rows are not
-contiguous is copied first.
+contiguous is copied first, on every call: of a matrix that is a transposed view, pass what it is a view of with the other
+layout.
 """
 from __future__ import annotations
 
