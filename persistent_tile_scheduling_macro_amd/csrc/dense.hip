@@ -268,7 +268,8 @@ int check(pgemm_ctx* h, int64_t M, int64_t N, int64_t K, int layout, int act, in
   if (gated != 0 && gated != 1) return fail(h, PGEMM_ERR_INVALID_ARG, "gated is %d, not 0 or 1", gated);
   if (dtype != PGEMM_F16 && dtype != PGEMM_BF16) return fail(h, PGEMM_ERR_INVALID_ARG, "dtype %d is not fp16 or bf16", dtype);
   if (M > kMaxSize || N > kMaxSize || K > kMaxSize) return fail(h, PGEMM_ERR_UNSUPPORTED, "sizes must not exceed 2^30");
-  // tiles of 128 x 64 in one launch of 2^32 threads, in 16 pieces; rows that a tile's offsets span
+  // 2^21 tiles of 64 x 128, 512 threads each, where a launch takes 2^32 threads (more pieces than one only up to 1024
+  // workgroups); rows that a tile's offsets span
   const int64_t C = gated ? 2 * N : N;
   auto tiles = [](int64_t a, int64_t b) { return ((a + 63) / 64) * ((b + 127) / 128); };
   if (tiles(M, C) > (1 << 21) || tiles(M, K) > (1 << 21) || tiles(C, K) > (1 << 21) || C > kMaxDirectStride || K > kMaxDirectStride)
