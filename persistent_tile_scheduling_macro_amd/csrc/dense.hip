@@ -39,9 +39,9 @@ struct Plan { int body; int split; double time; };
 struct Tile { int bm, bn; };
 Tile tile_of(int body) { return body == dense::kPing ? Tile{256, 256} : body == dense::kTile64 ? Tile{64, 128} : Tile{128, 128}; }
 
-// The bodies' times in us on 256 CUs, fitted to some 2900 measured calls of 1 .. 8192 rows and 64 .. 8192 columns and sums
-// (replayed from a graph, bf16, operands changing from call to call); the rule below was 2% slower than the best of them
-// in the geometric mean, 36% at worst. Examples (the times of few, tile 64, tile 128, pair, ping-pong, each with its
+// The bodies' times in us on 256 CUs, fitted to 2878 measured calls at 240 sizes of 1 .. 8192 rows and 64 .. 8192 columns and
+// sums (replayed from a graph, bf16, operands changing from call to call; all of them in profiles/dense_layer_rules.txt); the
+// rule below was 2% slower than the fastest in the geometric mean, 36% at worst. Examples (the times of few, tile 64, tile 128, pair, ping-pong, each with its
 // best number of pieces): 24 x 4096 x 4096 9, 14, 16, 18, 27; 512 x 4096 x 8192 -, 71, 43, 53, 59; 4099 x 2056 x 1024
 // -, -, 36, 31, 36; 8192 x 8192 x 4096 -, -, 615, 545, 455.
 //
@@ -129,8 +129,9 @@ Plan plan_grad(int64_t R, int64_t I, int64_t J) {
 
 // Both products of a backward pass, dx [M][K] over C and dw over M, as tiles of 128 x 128 in one launch, if that is faster
 // than one after the other (the second launch waits some 3 us for the first to drain). The workgroups are laid on the
-// card's slots as the hardware does, the longer ones first. Over 40 calls of 128 .. 8192 rows, 64 .. 4096 columns the rule
-// was 2% slower than the best body and pieces in the geometric mean, 21% at worst; two launches were 32% slower.
+// card's slots as the hardware does, the longer ones first. Over 40 sizes of 128 .. 8192 rows, 88 .. 3725 columns the
+// gradients took with the rule 2% longer than with the best body and pieces in the geometric mean, 18% at worst, in two
+// launches 31% (profiles/dense_layer_rules.txt).
 struct Both { int body, split_x, split_w; bool dw_first; };
 bool plan_both(int64_t M, int64_t K, int64_t C, bool nk, const Plan& dx, const Plan& dw, Both* best) {
   if (dx.body <= dense::kFew32) return false;
@@ -178,7 +179,9 @@ bool plan_both(int64_t M, int64_t K, int64_t C, bool nk, const Plan& dx, const P
   }
   return found;
 }
-// One of them by itself: 128 x 128 tiles with as many pieces (all such bodies add a piece's products in the same order).
+// One of them by itself: 128 x 128 tiles with as many pieces (all such bodies add a piece's products in the same order), so that
+// its values do not depend on whether the other is asked for. Over 37 sizes dx takes 5% longer for it than with its own best body
+// and pieces (512 x 1024 x 1024: 12.8 us for 10.1 with tiles of 64 x 128, the worst), dw 1% (11% at worst).
 Plan one_of(int64_t rows, int64_t columns, int64_t sum, int pieces) {
   const double one = tile_time(dense::kTile128, rows, columns, sum, pieces), two = tile_time(dense::kTile128Pair, rows, columns, sum, pieces);
   return {one < two ? (int)dense::kTile128 : (int)dense::kTile128Pair, pieces, one < two ? one : two};

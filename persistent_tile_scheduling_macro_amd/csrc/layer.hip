@@ -112,6 +112,8 @@ int pgemm_moe_layer(pgemm_handle_t h, const void* x, int64_t ldx, const void* id
     a.most = (int)q.most;
     a.sharers = (int)(q.sharers < p.sharers ? q.sharers : p.sharers);
     const int64_t tiles = (I + 15) / 16, fill = (512 + a.most - 1) / a.most; // two workgroups a CU
+    // Several turns of columns a workgroup for short rows. Measured at 45 sizes (profiles/dense_layer_rules.txt): up to H = 1024
+    // one turn each is from 14% faster to 40% slower, 4% slower in the mean; past it several are from 2% faster to 21% slower.
     const bool loop = H <= 1024 && fill < tiles;
     e = enqueue(h->stream, dim3((unsigned)(loop ? fill : tiles), (unsigned)a.most), dim3(512),
                 f16 ? layer::up_f16(gated, blocks, loop) : layer::up_bf16(gated, blocks, loop), a);
