@@ -10,8 +10,9 @@
 // lane's four outputs are columns of one row of y. Bias and residual are read
 // before the loop.
 //
-// 1 x 4096 x 4096 bf16: 8.0 us, 4.1 TB/s, of which a bare launch is 3.9; 16 x 4096
-// x 2 * 8192 gated fp16: 24.6 us, 5.5 TB/s.
+// 1 x 4096 x 4096 bf16: 8.0 us a call among others, 4.2 TB/s, of which a bare
+// launch is 3.9 (8.7 between the kernel's own timestamps); 16 x 4096 x 2 * 8192
+// gated fp16: 24.2 us for the kernel, 5.6 TB/s, 26.7 a call.
 #pragma once
 
 #include "dense.h"
@@ -32,7 +33,9 @@ __global__ void __launch_bounds__(WAVES * 64, BLK == 8 ? 2 : 4) few_kernel(Args 
   constexpr int STEP = NK ? 64 : 32, H = STEP / 32;
   constexpr int ROW = STEP * 2, LPR = ROW / 16, RPL = 64 / LPR; // bytes of a step's row, lanes to a row, rows of a load
   constexpr int L = 16 / RPL, XL = ROWS < 16 && RPL == 8 ? 1 : MB * L; // loads of 16 rows; loads of x
-  constexpr int D = !NK || GATED || ROWS > 16 ? 2 : 4; // steps in flight: 16 x 4096 x 8192 gated 26.8 us, with three 28.7; 1 x 4096 x 4096 9.1, with two 9.7
+  // Steps in flight. Calls replayed over six matrices in turn: 16 x 4096 x 2 * 8192 gated fp16 28.8 us, with three 30.7; 1 x 4096 x
+  // 4096 bf16 7.8, with two 8.0.
+  constexpr int D = !NK || GATED || ROWS > 16 ? 2 : 4;
   constexpr int OUT = GATED ? BLK / 2 : BLK; // blocks of y's columns
   typedef typename fast::Frag<DT>::t frag_t;
   typedef typename Traits<DT>::out_t out_t;

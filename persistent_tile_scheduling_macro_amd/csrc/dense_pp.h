@@ -12,11 +12,11 @@
 // wave a SIMD in it and the other group waiting, the training step of 8192 x 8192
 // x 4096 took 1498 us and that of 4096 x 4096 x 2048 gated 428, now 1425 and 410.
 //
-// 8192 x 8192 x 4096 bf16: the product with gelu and z 479 us, dx 459 and dW 495
-// (1150, 1200 and 1110 TFLOP/s; a plain library product in the same call 1130),
-// MFMA busy 0.55 to 0.60 at the clock that power leaves. A body of four waves with 128 x
-// 128 each, which reads a third less from LDS, took 543 us for 8192 x 4096 x 8192,
-// where this took 497.
+// 8192 x 8192 x 4096 bf16: the product with gelu and z 479 to 503 us, dx 459 to 484
+// and dW 495 to 513 (at best 1150, 1200 and 1110 TFLOP/s; a plain library product
+// in the same call 1130), MFMA busy 0.55 to 0.61 at the clock that power leaves. A
+// body of four waves with 128 x 128 each, which reads a third less from LDS, took
+// 543 us for 8192 x 4096 x 8192, where this took 497.
 #pragma once
 
 #include "dense.h"

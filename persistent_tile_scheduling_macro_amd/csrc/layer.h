@@ -28,8 +28,8 @@
 // value that is rounded (to 16 bits: it is an MFMA operand; bf16 outputs are off
 // by 0.0023 instead of one rounding's 0.0017).
 //
-// 32 tokens, 4 of 32 experts, 4096 x 2048 gated bf16: 182 and 117 us, 5.9 and 4.6
-// TB/s; one token, 8 of 64, 2048 x 1024 gated: 17 to 20 and 10 us, of each 3.9 the
+// 32 tokens, 4 of 32 experts, 4096 x 2048 gated bf16: 182 and 122 us, 6.0 and 4.4
+// TB/s; one token, 8 of 64, 2048 x 1024 gated: 20 and 10 us, of each 3.9 the
 // launch.
 #pragma once
 

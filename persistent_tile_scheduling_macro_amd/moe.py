@@ -190,10 +190,12 @@ def layer(x, ids, weights, w_in, w_out, *, act: str = "silu", gated: bool = True
     x [T, H]; ids int32 or int64 [T, k] (outside [0, E): dropped); weights float32 [T, k]; a(x) = act(x @ w_in[e].T) with
     w_in [E, I, H], or, gated, w_in [E, 2I, H] and act of the first I columns times the others; w_out [E, H, I]; act as
     in ``dense.matmul``. Each expert that a token names is read once for 64 tokens (up to four times where most of them
-    name it), so it is for the few tokens of a decoding batch; it takes up to 4096. Matrices that are not contiguous are
-    copied whole on every call. The ids of all tokens fix the order of the sums: a batch's results are always the same,
-    but a token's last bits may depend on the tokens beside it. For serving: it records no gradient, and refuses
-    arguments that want one.
+    name it), so it is for the few tokens of a decoding batch. It takes up to 4096, but more than 64 read the matrices
+    again: with 8 of 64 experts of 2048 x 1024 ``dispatch``, ``grouped_matmul`` and ``combine`` with torch's operations
+    between them are as fast at 64 tokens (192 us) and take 222 us for 128, where this takes 384. Matrices that are not
+    contiguous are copied whole on every call. The ids of all tokens fix the order of the sums: a batch's results are
+    always the same, but a token's last bits may depend on the tokens beside it. For serving: it records no gradient, and
+    refuses arguments that want one.
     """
     if torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, w_in, w_out)):
         raise ValueError("moe.layer has no gradient: call it under torch.no_grad() or on detached tensors")
